@@ -341,6 +341,101 @@ SAS_API sas_status sas_decode_select_scored(const sas_params* p, const sas_bf16*
                                             void* stream);
 
 /* ---------------------------------------------------------------------------
+ * KV cache in 4 bits. The pages have no counterpart: a serving cache at 5 bits
+ * a value instead of 16, for more or longer sequences per GPU and fewer bytes
+ * per decode step.
+ *
+ * The d channels of a token are cut into groups of 32. A group x keeps its
+ * minimum m = min x and a step s, both bf16, and a 4-bit code per channel:
+ *   s = bf16((max x − m) / 15), 0 if that is below 2^-126,
+ *   code = floor((x − m) / s + 1/2) in 0..15 (0 where s = 0),
+ * and stands for the values s·code + m, each within s/2 of x. A group whose
+ * range max − min is not a finite fp32 number (it holds a NaN or an infinity,
+ * or overflows) is stored as s = 0, m = NaN and reads as NaN throughout. A
+ * minimum of zero is stored as +0.
+ *
+ * One record holds 64 tokens (a block) of one KV head, of K or of V, in
+ * SAS_KV4_RECORD_BYTES(d) bytes. A record is 4 tiles of 16 tokens. With
+ * NG = d / 32 groups, a tile is 8 d bytes of codes, then 16·NG steps, then
+ * 16·NG minima. Codes are packed in little-endian 32-bit words, nibble 0 the
+ * lowest:
+ *   K codes: word [token][t 0..3][group j]; nibble p is channel 32 j + 8 t + p.
+ *   K steps, K minima: [token][group].
+ *   V codes: word [u 0..1][g 0..7][t 0..3][group j]; the low half is token
+ *            8u + 2t of the tile and the high half token 8u + 2t + 1; nibble p
+ *            of a half is channel 32 j + 4 g + p.
+ *   V steps: [t 0..3][group][i 0..3], token 8 (i / 2) + 2 t + i % 2.
+ *   V minima: [token][group].
+ * ------------------------------------------------------------------------- */
+
+#define SAS_KV4_GROUP 32
+#define SAS_KV4_RECORD_BYTES(d) (40 * (d))
+
+/* A caller-owned cache. Dense: block_table NULL, k and v are
+ * [B, Hkv, NKB, record] with NKB = seq_len / 64 (n_pages is not read). Paged:
+ * k and v are [n_pages, Hkv, record] and block_table int32 [B, NKB] gives the
+ * page of logical block m of sequence b, as in sas_decode_paged. Only the
+ * table entries of the blocks that a call touches are read. An entry outside
+ * [0, n_pages) raises SAS_ERR_DEVICE_INDEX and its block is left out: not
+ * written, not read, not attended to. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  const int32_t* block_table;
+  int n_pages;
+} sas_kv4_cache;
+
+/* Quantises new tokens into the cache, at the end of each sequence.
+ *   n_tokens   T, 1..seq_len: rows of k and v per sequence and head.
+ *   k, v       bf16 [B, Hkv, T, d]
+ *   cache_len  int32 [B]: tokens in each sequence's cache, the new ones
+ *              included.
+ *   new_len    int32 [B], or NULL for T each: sequence b brings n = new_len[b]
+ *              tokens, 0 <= n <= T. Row i < n goes to position
+ *              cache_len[b] − n + i. Rows i >= n are not read.
+ * Lengths that break 0 <= n <= T or n <= cache_len[b] <= seq_len raise
+ * SAS_ERR_DEVICE_INDEX, and nothing is written for that sequence. Tokens at
+ * other positions keep their bits. Two sequences must not write to one page
+ * position in the same call. */
+SAS_API sas_status sas_kv4_write(const sas_params* p, const sas_kv4_cache* cache, int n_tokens, const sas_bf16* k,
+                                 const sas_bf16* v, const int32_t* cache_len, const int32_t* new_len, void* stream);
+
+/* Reads back the tokens that sas_kv4_write wrote under the same n_tokens,
+ * cache_len and new_len, as bf16(s·code + m). With n_tokens = seq_len and
+ * new_len = cache_len the whole cache is read.
+ *   k, v  bf16 [B, Hkv, T, d]. Outputs; either may be NULL. Rows i >= n, and
+ *         the rows of a block with a bad table entry, are left as they were. */
+SAS_API sas_status sas_kv4_read(const sas_params* p, const sas_kv4_cache* cache, int n_tokens, sas_bf16* k,
+                                sas_bf16* v, const int32_t* cache_len, const int32_t* new_len, void* stream);
+
+/* Block-mean keys of the blocks that the last new_len[b] (NULL: n_tokens)
+ * tokens completed, from the cache's K values, summed in fp32 and rounded once
+ * to bf16: every block m with cache_len[b] − n < 64 (m + 1) <= cache_len[b].
+ * After each sas_kv4_write with the same lengths this keeps kmean current:
+ * n = 1 is the decode update, n = cache_len summarises a whole prompt. The
+ * length rules are those of sas_kv4_write.
+ *   kmean  bf16 [B, Hkv, NKB, d], as sas_block_mean_keys writes it. Other
+ *          blocks' entries are left as they were. */
+SAS_API sas_status sas_kv4_block_mean_keys(const sas_params* p, const sas_kv4_cache* cache, int n_tokens,
+                                           const int32_t* cache_len, const int32_t* new_len, sas_bf16* kmean,
+                                           void* stream);
+
+/* sas_decode over the 4-bit cache, dense or paged: the same block list, gate
+ * modes, splits and outputs, merged by sas_decode_combine. The cache's values
+ * s·code + m enter the products unrounded. The logits are exact to fp32, and
+ * P·s is rounded to 11 bits for P·V. */
+SAS_API sas_status sas_decode_kv4(const sas_params* p, const sas_bf16* q, const sas_kv4_cache* cache,
+                                  const int32_t* cache_len, const float* s, const int32_t* idx, const float* lse_s,
+                                  int n_split, float* o_part, float* lse_part, void* stream);
+
+/* sas_decode_fused over the 4-bit cache, dense or paged: select, attention and
+ * merge in one launch, with the outputs and limits (G <= 8, K <= 255,
+ * NKB <= 2048) of sas_decode_fused. */
+SAS_API sas_status sas_decode_fused_kv4(const sas_params* p, const sas_bf16* q, const sas_kv4_cache* cache,
+                                        const int32_t* cache_len, const float* s, int32_t* idx, float* lse_s,
+                                        sas_bf16* o, float* lse_o, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Decode step that allocates nothing. The paper has no counterpart to this
  * entry point; it exists for callers of this library that cannot allocate.
  * ------------------------------------------------------------------------- */

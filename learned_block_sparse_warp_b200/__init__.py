@@ -9,7 +9,9 @@ when the library has not been built (``python -m learned_block_sparse_warp_b200.
 The entry points and their contracts are those of include/sas.h:
 ``sas_topk_select``, ``sas_gate_lse``, ``sas_fwd``, ``sas_bwd``
 (+ ``sas_bwd_workspace_size``), ``sas_decode``, ``sas_decode_combine``,
-``sas_get_device_error``.
+``sas_get_device_error``. The 4-bit KV cache has ``Kv4Cache``, ``sas_kv4_write``,
+``sas_kv4_read``, ``sas_kv4_block_mean_keys``, ``sas_decode_kv4`` and
+``sas_decode_fused_kv4``.
 """
 from __future__ import annotations
 
@@ -29,7 +31,9 @@ __all__ = [
     "sas_version",
     "DecodeGraph", "sas_selftest_wait_timeout", "sas_block_mean_keys", "sas_decode_select_scored",
     "decode_step_scored", "sas_train_steps_host", "empty_device_slot", "sas_decode_fused", "sas_decode_fused_paged",
-    "decode_step_fused",
+    "decode_step_fused", "SAS_KV4_GROUP", "Kv4Cache", "kv4_record_bytes", "empty_kv4_cache", "sas_kv4_write",
+    "sas_kv4_read", "sas_kv4_block_mean_keys", "sas_decode_kv4", "sas_decode_fused_kv4", "decode_step_kv4",
+    "decode_step_fused_kv4", "decode_step_scored_kv4",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsas_b200.so")
@@ -42,6 +46,7 @@ SAS_GATE_SOFTMAX_OUTSIDE = 4  # ablation: g = softmax(s) weights the values afte
 STATUS = {0: "SAS_OK", 1: "SAS_ERR_INVALID_ARG", 2: "SAS_ERR_UNSUPPORTED", 3: "SAS_ERR_WORKSPACE",
           4: "SAS_ERR_CUDA", 5: "SAS_ERR_TIMEOUT", 6: "SAS_ERR_DEVICE_INDEX"}
 BLOCK = 64
+SAS_KV4_GROUP = 32  # channels that share a step and a minimum in the 4-bit cache
 
 
 class SasError(RuntimeError):
@@ -69,12 +74,19 @@ class sas_params(ctypes.Structure):
     ]
 
 
+class sas_kv4_cache(ctypes.Structure):
+    """Mirror of ``sas_kv4_cache``: the records of K and V, and the block table of a paged cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m learned_block_sparse_warp_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(sas_params)
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    C = ctypes.POINTER(sas_kv4_cache)
     sig = {
         "sas_topk_select": [P, vp, vp, vp, vp, vp],
         "sas_gate_lse": [P, vp, vp, vp, vp],
@@ -93,6 +105,11 @@ def _load() -> ctypes.CDLL:
         "sas_block_mean_keys": [P, vp, vp, vp, vp],
         "sas_decode_select_scored": [P, vp, vp, vp, vp, vp, vp, vp],
         "sas_train_steps_host": [P, ctypes.c_int, ctypes.POINTER(sas_host_step), ctypes.POINTER(sas_device_slot), vp],
+        "sas_kv4_write": [P, C, ctypes.c_int, vp, vp, vp, vp, vp],
+        "sas_kv4_read": [P, C, ctypes.c_int, vp, vp, vp, vp, vp],
+        "sas_kv4_block_mean_keys": [P, C, ctypes.c_int, vp, vp, vp, vp],
+        "sas_decode_kv4": [P, vp, C, vp, vp, vp, vp, ctypes.c_int, vp, vp, vp],
+        "sas_decode_fused_kv4": [P, vp, C, vp, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -356,6 +373,130 @@ def sas_train_steps_host(p: Params, steps, slots, stream=None) -> None:
                                                             _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# KV cache in 4 bits
+# ---------------------------------------------------------------------------
+def kv4_record_bytes(head_dim: int) -> int:
+    """Bytes of one record: 64 tokens of one KV head, K or V (5 bits a value)."""
+    return 40 * head_dim
+
+
+def _arg(t, dtype, shape, name: str, dev: int):
+    """Pointer of a tensor of the call, checked; dev is the current device, which the launch goes to."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: expected a CUDA tensor on the current device cuda:{dev}, got {t.device}")
+        _ptr(t, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, name: str, dev: int):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+class Kv4Cache:
+    """A 4-bit KV cache over the caller's uint8 tensors (the format is in include/sas.h).
+
+    Dense: k and v are [B, Hkv, NKB, 40 d]. Paged: [n_pages, Hkv, 40 d], with block_table int32 [B, NKB]. The handle
+    keeps the tensors alive and may be used with any ``Params`` of the same batch, KV heads, head_dim and seq_len."""
+
+    __slots__ = ("k", "v", "block_table", "dims", "device", "_c", "_ref")
+
+    def __init__(self, p: Params, k: torch.Tensor, v: torch.Tensor, block_table: Optional[torch.Tensor] = None):
+        n_pages = 0
+        shape = (p.batch, p.n_kv_heads, p.n_blocks, kv4_record_bytes(p.head_dim))
+        if block_table is not None:
+            n_pages = int(k.shape[0])
+            shape = (n_pages, p.n_kv_heads, kv4_record_bytes(p.head_dim))
+        dev = k.get_device()
+        if dev < 0:
+            raise ValueError("k: expected a CUDA tensor")
+        self.k, self.v, self.block_table, self.device = k, v, block_table, dev
+        self.dims = (p.batch, p.n_kv_heads, p.head_dim, p.seq_len)
+        self._c = sas_kv4_cache(_arg(k, torch.uint8, shape, "k", dev), _arg(v, torch.uint8, shape, "v", dev),
+                                _opt(block_table, i32, (p.batch, p.n_blocks), "block_table", dev), n_pages)
+        self._ref = ctypes.byref(self._c)
+
+    def of(self, p: Params):
+        """The C struct, once p has been checked against the cache's shape and the current device."""
+        if self.dims != (p.batch, p.n_kv_heads, p.head_dim, p.seq_len):
+            raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self.dims}, called with "
+                             f"{(p.batch, p.n_kv_heads, p.head_dim, p.seq_len)}")
+        if self.device != torch.cuda.current_device():
+            raise ValueError(f"cache: lies on cuda:{self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return self._ref
+
+
+def empty_kv4_cache(p: Params, n_pages: Optional[int] = None, block_table: Optional[torch.Tensor] = None,
+                    device="cuda") -> Kv4Cache:
+    """An uninitialised cache: dense, or of n_pages pages reached through block_table (every value a decode step
+    reads is written by ``sas_kv4_write`` first)."""
+    if (n_pages is None) != (block_table is None):
+        raise ValueError("a paged cache takes n_pages and block_table, a dense one neither")
+    shape = (p.batch, p.n_kv_heads, p.n_blocks) if n_pages is None else (n_pages, p.n_kv_heads)
+    shape += (kv4_record_bytes(p.head_dim),)
+    return Kv4Cache(p, torch.empty(shape, dtype=torch.uint8, device=device),
+                    torch.empty(shape, dtype=torch.uint8, device=device), block_table)
+
+
+def sas_kv4_write(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
+    """Quantises k, v [B, Hkv, T, d] into the cache at positions cache_len - new_len .. cache_len - 1 (new_len: T)."""
+    c, dev, T = cache.of(p), cache.device, k.shape[2]
+    sh = (p.batch, p.n_kv_heads, T, p.head_dim)
+    _check("sas_kv4_write", lib.sas_kv4_write(
+        p.c(), c, T, _arg(k, bf16, sh, "k", dev), _arg(v, bf16, sh, "v", dev),
+        _arg(cache_len, i32, (p.batch,), "cache_len", dev), _opt(new_len, i32, (p.batch,), "new_len", dev),
+        _stream(stream)))
+
+
+def sas_kv4_read(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
+    """Reads back what ``sas_kv4_write`` wrote under the same lengths into k, v [B, Hkv, T, d] (either may be None)."""
+    c, dev = cache.of(p), cache.device
+    if k is None and v is None:
+        raise ValueError("k, v: at least one output is needed")
+    T = (v if k is None else k).shape[2]
+    sh = (p.batch, p.n_kv_heads, T, p.head_dim)
+    _check("sas_kv4_read", lib.sas_kv4_read(
+        p.c(), c, T, _opt(k, bf16, sh, "k", dev), _opt(v, bf16, sh, "v", dev),
+        _arg(cache_len, i32, (p.batch,), "cache_len", dev), _opt(new_len, i32, (p.batch,), "new_len", dev),
+        _stream(stream)))
+
+
+def sas_kv4_block_mean_keys(p: Params, cache: Kv4Cache, n_tokens: int, cache_len, kmean, new_len=None,
+                            stream=None) -> None:
+    """Block means of the blocks that the last new_len (default n_tokens) tokens completed, into kmean [B, Hkv, NKB, d]."""
+    c, dev = cache.of(p), cache.device
+    _check("sas_kv4_block_mean_keys", lib.sas_kv4_block_mean_keys(
+        p.c(), c, n_tokens, _arg(cache_len, i32, (p.batch,), "cache_len", dev),
+        _opt(new_len, i32, (p.batch,), "new_len", dev),
+        _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", dev), _stream(stream)))
+
+
+def sas_decode_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, idx, lse_s, n_split: int, o_part, lse_part,
+                   stream=None) -> None:
+    """sas_decode over a 4-bit cache."""
+    c, dev = cache.of(p), cache.device
+    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+    _check("sas_decode_kv4", lib.sas_decode_kv4(
+        p.c(), _arg(q, bf16, (B, Hq, d), "q", dev), c, _arg(cache_len, i32, (B,), "cache_len", dev),
+        _opt(s, f32, (B, Hkv, p.n_blocks), "s", dev), _arg(idx, i32, (B, Hkv, p.top_k), "idx", dev),
+        _opt(lse_s, f32, (B, Hkv), "lse_s", dev), n_split, _arg(o_part, f32, (B, Hq, n_split, d), "o_part", dev),
+        _arg(lse_part, f32, (B, Hq, n_split), "lse_part", dev), _stream(stream)))
+
+
+def sas_decode_fused_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, o, idx=None, lse_s=None, lse_o=None,
+                         stream=None) -> None:
+    """sas_decode_fused over a 4-bit cache: select, attention and merge in one launch."""
+    c, dev = cache.of(p), cache.device
+    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+    _check("sas_decode_fused_kv4", lib.sas_decode_fused_kv4(
+        p.c(), _arg(q, bf16, (B, Hq, d), "q", dev), c, _arg(cache_len, i32, (B,), "cache_len", dev),
+        _arg(s, f32, (B, Hkv, p.n_blocks), "s", dev), _opt(idx, i32, (B, Hkv, p.top_k), "idx", dev),
+        _opt(lse_s, f32, (B, Hkv), "lse_s", dev), _arg(o, bf16, (B, Hq, d), "o", dev),
+        _opt(lse_o, f32, (B, Hq), "lse_o", dev), _stream(stream)))
+
+
 def sas_selftest_wait_timeout(stream=None) -> None:
     """One bounded wait that runs out (about a second); sas_get_device_error then reads SAS_ERR_TIMEOUT."""
     _check("sas_selftest_wait_timeout", lib.sas_selftest_wait_timeout(_stream(stream)))
@@ -453,6 +594,34 @@ def decode_step_scored(p: Params, q, kc, vc, kmean, cache_len, s, n_split: int, 
     sas_decode_select_scored(p, q, kmean, cache_len, s, out["idx"], out["lse_s"], stream=stream)
     sas_decode(p, q, kc, vc, cache_len, s, out["idx"], out["lse_s"], n_split, out["o_part"], out["lse_part"],
                stream=stream)
+    sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
+
+
+def decode_step_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, stream=None) -> None:
+    """One decode step over a 4-bit cache: Top-K select (decode form), split-K attention, LSE merge."""
+    sas_topk_select(p, s, out["idx"], out["lse_s"], cache_len=cache_len, stream=stream)
+    sas_decode_kv4(p, q, cache, cache_len, s, out["idx"], out["lse_s"], n_split, out["o_part"], out["lse_part"],
+                   stream=stream)
+    sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
+
+
+def decode_step_fused_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, out: dict, stream=None) -> None:
+    """One decode step over a 4-bit cache in one launch; fills out["o"], and out["lse_o"], out["idx"] and
+    out["lse_s"] when present."""
+    sas_decode_fused_kv4(p, q, cache, cache_len, s, out["o"], idx=out.get("idx"), lse_s=out.get("lse_s"),
+                         lse_o=out.get("lse_o"), stream=stream)
+
+
+def decode_step_scored_kv4(p: Params, q, k_new, v_new, cache: Kv4Cache, kmean, cache_len, s, n_split: int, out: dict,
+                           stream=None) -> None:
+    """A whole serving step over a 4-bit cache that scores its own history: write the new token (k_new, v_new
+    [B, Hkv, 1, d], at position cache_len - 1), update the block means of the blocks it completed, score and
+    select in one launch (s is written), split-K attention, merge."""
+    sas_kv4_write(p, cache, k_new, v_new, cache_len, stream=stream)
+    sas_kv4_block_mean_keys(p, cache, 1, cache_len, kmean, stream=stream)
+    sas_decode_select_scored(p, q, kmean, cache_len, s, out["idx"], out["lse_s"], stream=stream)
+    sas_decode_kv4(p, q, cache, cache_len, s, out["idx"], out["lse_s"], n_split, out["o_part"], out["lse_part"],
+                   stream=stream)
     sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
 
 
