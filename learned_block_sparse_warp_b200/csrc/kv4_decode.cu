@@ -38,7 +38,11 @@ using namespace kv4;
 namespace {
 
 constexpr int kWarps = dec::kThreads / 32;
-constexpr int kSlots = 3;           // record slots of a warp's ring
+#ifndef KV4_OCC
+#define KV4_OCC 3
+#define KV4_SLOTS 3
+#endif
+constexpr int kSlots = KV4_SLOTS;           // record slots of a warp's ring
 constexpr int kMaxTasks = 256;      // blocks of one CTA's list (fused: the whole list of a row)
 constexpr float kPShift = 8.f;      // P is kept times 2^8
 constexpr int kStepField = 17;      // exponent field that the largest step gets in fp16 when the base is set
@@ -70,6 +74,14 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
@@ -84,6 +96,23 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t y;
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
   return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+      "add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ float exp2_approx(float x) {  // 2^x, relative error about 2^-22, 0 below 2^-126
   float y;
@@ -135,7 +164,9 @@ struct Query {
   static constexpr int NG = D / kGroup;
   uint32_t b[NG][2][2];  // channels 32 j + 8 t + {0, 4}, {1, 5}/16; {2, 6}, {3, 7}/16
   uint32_t sum[2];       // part t of Σ q_j (three bf16 parts, and 0), groups 0, 1 and 2, 3
-  float fa[2], fb[2];    // z = S · fa · fb for heads 2t and 2t + 1
+  float2 f;              // logit (log2 units) = S · f for heads 2t and 2t + 1
+  float2 over;           // factors of S before f where f alone would leave fp32's range (queries above 2^100)
+  bool big;              // whether any head of the row has one
 
   __device__ __forceinline__ void load(const uint16_t* q, int G, float scale) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -179,12 +210,11 @@ struct Query {
     }
     sum[0] = pack_bf16x2(part[0], part[1]);
     sum[1] = NG == 4 ? pack_bf16x2(part[NG - 2], part[NG - 1]) : 0u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int eh = __shfl_sync(0xffffffffu, e, 8 * t + 4 * i);
-      fa[i] = scale * kLog2e * 512.f;  // 2^24 / 2^15
-      fb[i] = ldexpf(1.f, eh);
-    }
+    const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+    const float c = scale * kLog2e * 512.f;  // 2^24 / 2^15
+    f = make_float2(c * ldexpf(1.f, min(e0, 100)), c * ldexpf(1.f, min(e1, 100)));
+    over = make_float2(ldexpf(1.f, max(e0 - 100, 0)), ldexpf(1.f, max(e1 - 100, 0)));
+    big = __any_sync(0xffffffffu, e > 100);
   }
 };
 
@@ -195,7 +225,7 @@ template <int D>
 struct State {
   static constexpr int NG = D / kGroup;
   float acc[NG][2][4];
-  float accm[NG][2];  // Σ p m over this lane's tokens
+  float2 accm[NG];    // Σ p m over this lane's tokens, heads 2t and 2t + 1
   float m[2], l[2];   // maximum (log2), and Σ p 2^8 over this lane's tokens
   uint32_t lo;        // base of the steps' exponent field, as bf16 bits in both halves
   uint32_t lim;       // largest step bits below the limit, in both halves
@@ -205,7 +235,7 @@ struct State {
     for (int j = 0; j < NG; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
-      accm[j][0] = accm[j][1] = 0.f;
+      accm[j] = make_float2(0.f, 0.f);
     }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
@@ -213,74 +243,89 @@ struct State {
   }
 };
 
-// S of a block's 64 tokens from its K record, as logits in log2 units.
-template <int D>
-__device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& q, int ntok, float lam,
-                                            float (&z)[kTiles][4]) {
+// S of a block's 64 tokens from its K record. With FULL, all of them count;
+// otherwise those past ntok become -inf.
+template <int D, bool FULL>
+__device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& q, int ntok, float2 (&S)[kTiles][2]) {
   using F = Fmt<D>;
   constexpr int NG = F::NG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    if (16 * i >= ntok) {
-      z[i][0] = z[i][1] = z[i][2] = z[i][3] = -INFINITY;
+    if (!FULL && 16 * i >= ntok) {
+      S[i][0] = S[i][1] = make_float2(-INFINITY, -INFINITY);
       continue;
     }
     const uint8_t* tile = rec + i * F::kTileBytes;
     const Words<NG> w0 = lds_words<NG>(tile + F::k_word(g, t, 0)), w1 = lds_words<NG>(tile + F::k_word(g + 8, t, 0));
     const Words<NG / 2> s0 = lds_params<NG>(tile + F::k_step(g, 0)), s1 = lds_params<NG>(tile + F::k_step(g + 8, 0));
     const Words<NG / 2> m0 = lds_params<NG>(tile + F::min_at(g, 0)), m1 = lds_params<NG>(tile + F::min_at(g + 8, 0));
-    float S[4] = {0.f, 0.f, 0.f, 0.f};
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
     const uint32_t am[4] = {m0.w[0], m1.w[0], NG == 4 ? m0.w[NG / 2 - 1] : 0u, NG == 4 ? m1.w[NG / 2 - 1] : 0u};
-    mma_bf16_16816(S, am, q.sum[0], q.sum[1]);
+    mma_bf16_16816(x, am, q.sum[0], q.sum[1]);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[4];
       const uint32_t a = w0.w[j], b = w1.w[j], a8 = a >> 8, b8 = b >> 8;
-      mma_f16(c, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.b[j][0][0], q.b[j][0][1]);
+      mma_f16_zero(c, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.b[j][0][0], q.b[j][0][1]);
       mma_f16(c, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.b[j][1][0], q.b[j][1][1]);
-      const float x0 = bf16_of(s0, j), x1 = bf16_of(s1, j);
-      S[0] = fmaf(c[0], x0, S[0]);
-      S[1] = fmaf(c[1], x0, S[1]);
-      S[2] = fmaf(c[2], x1, S[2]);
-      S[3] = fmaf(c[3], x1, S[3]);
+      const float y0 = bf16_of(s0, j), y1 = bf16_of(s1, j);
+      x[0] = fmaf(c[0], y0, x[0]);
+      x[1] = fmaf(c[1], y0, x[1]);
+      x[2] = fmaf(c[2], y1, x[2]);
+      x[3] = fmaf(c[3], y1, x[3]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[i][e] = fmaf(S[e] * q.fa[e & 1], q.fb[e & 1], lam);
-    if (16 * i + 16 > ntok) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[i][e] = 16 * i + g + 8 * (e >> 1) < ntok ? z[i][e] : -INFINITY;
+    if (q.big) {
+      x[0] *= q.over.x, x[1] *= q.over.y, x[2] *= q.over.x, x[3] *= q.over.y;
     }
+    if (!FULL && 16 * i + 16 > ntok) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = 16 * i + g + 8 * (e >> 1) < ntok ? x[e] : -INFINITY;
+    }
+    S[i][0] = make_float2(x[0], x[1]);
+    S[i][1] = make_float2(x[2], x[3]);
   }
 }
 
-// The online softmax: z becomes p · 2^8, and the state is rescaled.
+// The online softmax: S becomes p · 2^8 with p = 2^(S f + lam - max), and the
+// state is rescaled. (f > 0, so the largest logit is that of the largest S.)
 template <int D>
-__device__ __forceinline__ void softmax_block(State<D>& st, float (&z)[kTiles][4]) {
-  float sub[2], al[2];
+__device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[kTiles][2]) {
+  float top[2], sub[2], al[2];
+  top[0] = fmaxf(S[0][0].x, S[0][1].x);
+  top[1] = fmaxf(S[0][0].y, S[0][1].y);
+#pragma unroll
+  for (int i = 1; i < kTiles; ++i) {
+    top[0] = fmaxf(top[0], fmaxf(S[i][0].x, S[i][1].x));
+    top[1] = fmaxf(top[1], fmaxf(S[i][0].y, S[i][1].y));
+  }
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) {
+    top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+    top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float mx = st.m[h];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) mx = fmaxf(mx, fmaxf(z[i][h], z[i][2 + h]));
-#pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mx = fmaxf(st.m[h], fmaf(top[h], h ? q.f.y : q.f.x, lam));
     const float ref = mx == -INFINITY ? 0.f : mx;  // nothing but masked tokens so far: every p is 0
     al[h] = exp2_approx(st.m[h] - ref);
-    sub[h] = ref - kPShift;
+    sub[h] = lam - ref + kPShift;
     st.m[h] = mx;
   }
+  const float2 add = make_float2(sub[0], sub[1]);
+  float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[i][e] = exp2_approx(z[i][e] - sub[e & 1]);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) sum += z[i][h] + z[i][2 + h];
-    st.l[h] = fmaf(st.l[h], al[h], sum);
-  }
+    for (int u = 0; u < 2; ++u) {
+      float2 z = fma_f32x2(S[i][u], q.f, add);
+      z.x = exp2_approx(z.x);
+      z.y = exp2_approx(z.y);
+      S[i][u] = z;
+      sum = add_f32x2(sum, z);
+    }
+  st.l[0] = fmaf(st.l[0], al[0], sum.x);
+  st.l[1] = fmaf(st.l[1], al[1], sum.y);
   if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
     for (int j = 0; j < State<D>::NG; ++j) {
@@ -289,21 +334,21 @@ __device__ __forceinline__ void softmax_block(State<D>& st, float (&z)[kTiles][4
         st.acc[j][0][e] *= al[e & 1];
         st.acc[j][1][e] *= al[e & 1];
       }
-      st.accm[j][0] *= al[0];
-      st.accm[j][1] *= al[1];
+      st.accm[j].x *= al[0];
+      st.accm[j].y *= al[1];
     }
   }
 }
 
 // O += P V from the block's V record.
-template <int D>
-__device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, int ntok, const float (&p)[kTiles][4]) {
+template <int D, bool FULL>
+__device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, int ntok, const float2 (&p)[kTiles][2]) {
   using F = Fmt<D>;
   constexpr int NG = F::NG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    if (16 * i >= ntok) break;
+    if (!FULL && 16 * i >= ntok) break;
     const uint8_t* tile = rec + i * F::kTileBytes;
     uint32_t stp[NG][2];  // steps of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
@@ -313,7 +358,7 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
     }
     const Words<NG> w0 = lds_words<NG>(tile + F::v_half(2 * t, g, 0)), w1 = lds_words<NG>(tile + F::v_half(8 + 2 * t, g, 0));
     Words<NG / 2> m0 = lds_params<NG>(tile + F::min_at(g, 0)), m1 = lds_params<NG>(tile + F::min_at(g + 8, 0));
-    if (16 * i + 16 > ntok) {  // tokens past the end may hold anything: their p is 0, their steps and minima are made 0
+    if (!FULL && 16 * i + 16 > ntok) {  // tokens past the end may hold anything: their p is 0, and their steps and minima are made 0
       const int r = ntok - 16 * i;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -327,10 +372,10 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
         m1.w[j] = g + 8 < r ? m1.w[j] : 0u;
       }
     }
-    uint32_t mx = 0;
+    uint32_t mx = st.lim;
 #pragma unroll
     for (int j = 0; j < NG; ++j) mx = __vmaxu2(mx, __vmaxu2(stp[j][0], stp[j][1]));
-    if (__any_sync(0xffffffffu, st.lim == 0u || __vmaxu2(mx, st.lim) != st.lim)) {  // the base of the steps moves up
+    if (__any_sync(0xffffffffu, mx != st.lim)) {  // a step past the limit, or the first that is not 0: the base moves up
       const uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
       const int old = int((st.lo & 0xffffu) >> 7), now = max(old, int(top >> 7) - kStepField);
       const float f = exp2_approx(float(old - now));
@@ -344,17 +389,19 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
       st.lo = uint32_t(now << 7) * 0x10001u;
       st.lim = uint32_t(((now + kStepLimit) << 7) - 1) * 0x10001u;
     }
-    const uint32_t p0 = transpose8x8(pack_f16x2(p[i][0], p[i][1])), p1 = transpose8x8(pack_f16x2(p[i][2], p[i][3]));
+    const uint32_t p0 = transpose8x8(pack_f16x2(p[i][0].x, p[i][0].y)), p1 = transpose8x8(pack_f16x2(p[i][1].x, p[i][1].y));
+    const uint32_t lo8 = 0u - 8u * st.lo;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      const uint32_t b0 = mul_f16x2(p0, (__vmaxu2(stp[j][0], st.lo) - st.lo) << 3);
-      const uint32_t b1 = mul_f16x2(p1, (__vmaxu2(stp[j][1], st.lo) - st.lo) << 3);
+      // (max(bits, lo) - lo) << 3 in both halves: the fp16 whose exponent field is the step's less lo's
+      const uint32_t b0 = mul_f16x2(p0, __vmaxu2(stp[j][0], st.lo) * 8u + lo8);
+      const uint32_t b1 = mul_f16x2(p1, __vmaxu2(stp[j][1], st.lo) * 8u + lo8);
       const uint32_t a = w0.w[j], b = w1.w[j], a8 = a >> 8, b8 = b >> 8;
       mma_f16(st.acc[j][0], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
       mma_f16(st.acc[j][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, b0, b1);
       const float x0 = bf16_of(m0, j), x1 = bf16_of(m1, j);
-      st.accm[j][0] = fmaf(p[i][2], x1, fmaf(p[i][0], x0, st.accm[j][0]));
-      st.accm[j][1] = fmaf(p[i][3], x1, fmaf(p[i][1], x0, st.accm[j][1]));
+      st.accm[j].x = fmaf(p[i][1].x, x1, fmaf(p[i][0].x, x0, st.accm[j].x));
+      st.accm[j].y = fmaf(p[i][1].y, x1, fmaf(p[i][0].y, x0, st.accm[j].y));
     }
   }
 }
@@ -362,15 +409,19 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
 // A warp's ring of records. Item 2 i is block i's K, item 2 i + 1 its V; an
 // item's slot is refilled as soon as it has been used.
 template <int D>
-__device__ __forceinline__ void ring_issue(uint8_t* ring, const Cache& c, int item, int rec, int ntok) {
+__device__ __forceinline__ void ring_issue(uint8_t* ring, const Cache& c, int item, int slot, int rec, int ntok) {
   using F = Fmt<D>;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(rec) * F::kRecord + lane * 16;
-  const uint32_t dst = smem_u32(ring) + (item % kSlots) * F::kRecord + lane * 16;
-  const int bytes = (ntok + kTile - 1) / kTile * F::kTileBytes;
+  const uint32_t dst = smem_u32(ring) + slot * F::kRecord + lane * 16;
+  if (ntok == kBlock) {
 #pragma unroll
-  for (int o = 0; o < F::kRecord; o += 512)
-    if (lane * 16 + o < bytes) cp_async16(dst + o, src + o);
+    for (int o = 0; o < F::kRecord; o += 512) cp_async16(dst + o, src + o);
+  } else {  // the tiles that hold tokens
+    const int bytes = (ntok + kTile - 1) / kTile * F::kTileBytes;
+#pragma unroll 1
+    for (int o = 0; o + lane * 16 < bytes; o += 512) cp_async16(dst + o, src + o);
+  }
 }
 
 // Runs a warp over blocks first, first + kWarps, ... < n of its CTA's list
@@ -381,38 +432,52 @@ __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st,
                                            const int* rec_s, const float* lam_s, int first, int n, int cur_at,
                                            int cur_ntok, int issued) {
   const int mine = n > first ? (n - 1 - first) / kWarps + 1 : 0;
-  auto issue = [&](int item) {
+  auto issue = [&](int item, int slot) {
     if (item < 2 * mine) {
       const int at = first + (item >> 1) * kWarps;
       const int rec = rec_s[at];
-      if (rec >= 0) ring_issue<D>(ring, a.c, item, rec, at == cur_at ? cur_ntok : kBlock);
+      if (rec >= 0) ring_issue<D>(ring, a.c, item, slot, rec, at == cur_at ? cur_ntok : kBlock);
     }
     cp_async_commit();
   };
-  for (int k = issued; k < kSlots; ++k) issue(k);
+  for (int k = issued; k < kSlots; ++k) issue(k, k);
+  int slot = 0;
+  auto next = [&] {
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+  };
   for (int i = 0; i < mine; ++i) {
-    const int at = first + i * kWarps, rec = rec_s[at];
-    const int ntok = rec < 0 ? 0 : at == cur_at ? cur_ntok : kBlock;
+    const int at = first + i * kWarps;
+    const int ntok = rec_s[at] < 0 ? 0 : at == cur_at ? cur_ntok : kBlock;
     const float lam = lam_s[at];
-    float z[kTiles][4];
+    float2 S[kTiles][2];
     cp_async_wait<kSlots - 1>();
     __syncwarp();
-    score_block<D>(ring + (2 * i) % kSlots * Fmt<D>::kRecord, q, ntok, a.outside ? 0.f : lam, z);
+    const uint8_t* rec = ring + slot * Fmt<D>::kRecord;
+    if (ntok == kBlock)
+      score_block<D, true>(rec, q, ntok, S);
+    else
+      score_block<D, false>(rec, q, ntok, S);
     __syncwarp();
-    issue(2 * i + kSlots);
-    softmax_block<D>(st, z);
+    issue(2 * i + kSlots, slot);
+    next();
+    softmax_block<D>(st, q, a.outside ? 0.f : lam, S);
     if (a.outside) {
       const float gw = exp2f(lam);
 #pragma unroll
       for (int k = 0; k < kTiles; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[k][e] *= gw;
+        for (int u = 0; u < 2; ++u) S[k][u] = make_float2(S[k][u].x * gw, S[k][u].y * gw);
     }
     cp_async_wait<kSlots - 1>();
     __syncwarp();
-    value_block<D>(ring + (2 * i + 1) % kSlots * Fmt<D>::kRecord, st, ntok, z);
+    rec = ring + slot * Fmt<D>::kRecord;
+    if (ntok == kBlock)
+      value_block<D, true>(rec, st, ntok, S);
+    else
+      value_block<D, false>(rec, st, ntok, S);
     __syncwarp();
-    issue(2 * i + 1 + kSlots);
+    issue(2 * i + 1 + kSlots, slot);
+    next();
   }
   cp_async_wait<0>();
 }
@@ -438,7 +503,7 @@ __device__ __forceinline__ void store_partial(const State<D>& st, Partial<D>* ou
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      float am = st.accm[j][h];
+      float am = h ? st.accm[j].y : st.accm[j].x;
 #pragma unroll
       for (int o = 4; o <= 16; o <<= 1) am += __shfl_xor_sync(0xffffffffu, am, o);
       am *= inv;
@@ -493,7 +558,7 @@ constexpr int smem_bytes() {
 
 // One CTA per (sequence, KV head, split).
 template <int D>
-__global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_split_kernel(Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_split_kernel(Kv4DecodeArgs a) {
   using F = Fmt<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int rec_s[kMaxDecodeBlocksPerSplit];
@@ -524,8 +589,9 @@ __global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_split_kernel(Kv4D
       else if (a.gated)
         lam = gate_lam2(a.gate, a.s[size_t(bh) * NB + m], a.lse_s_in != nullptr ? a.lse_s_in[bh] : 0.f);
     }
-    rec_s[tid] = m < 0 ? -1 : record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-    lam_s[tid] = lam;
+    const int rec = m < 0 ? -1 : record_of(a.c, b, h, m, a.Hkv, NB, a.err);
+    rec_s[tid] = rec;
+    lam_s[tid] = rec < 0 ? 0.f : lam;
   }
   Query<D> q;
   q.load(a.q + size_t(bh) * a.G * D, a.G, a.scale);
@@ -551,7 +617,7 @@ __global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_split_kernel(Kv4D
 // One cluster per (sequence, KV head): each CTA selects the row's blocks
 // itself and takes every CS-th one.
 template <int D>
-__global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
   using F = Fmt<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int sel_s[dec::kFusedMaxK];
@@ -594,7 +660,7 @@ __global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_fused_kernel(Kv4D
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (rec >= 0) ring_issue<D>(ring, a.c, k, rec, L - c * kBlock);
+      if (rec >= 0) ring_issue<D>(ring, a.c, k, k, rec, L - c * kBlock);
       cp_async_commit();
     }
     issued = 2;
@@ -629,8 +695,9 @@ __global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_fused_kernel(Kv4D
   auto place = [&](int pos, int m) {
     if (idx_row != nullptr) idx_row[pos - 1] = m;
     if (pos % CS == rank) {
-      rec_s[pos / CS] = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-      lam_s[pos / CS] = a.gated ? gate_lam2(a.gate, __ldg(srow + m), lse) : 0.f;
+      const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
+      rec_s[pos / CS] = rec;
+      lam_s[pos / CS] = a.gated && rec >= 0 ? gate_lam2(a.gate, __ldg(srow + m), lse) : 0.f;
     }
   };
   if (n == c) {
