@@ -622,30 +622,38 @@ __global__ void __launch_bounds__(dec::kThreads) decode_fused_kernel(DecodeFused
   cluster.sync();  // no CTA leaves while another may still read its partial
 }
 
-// One warp per (sequence, query head). The lanes read the split LSEs in
-// parallel and reduce them with shuffles. The partials are then streamed in
-// batches of 16 float4 (d = 128) or float2 (d = 64) loads per lane, all
-// issued before the first is used, so a batch costs one L2 round trip. The
-// weight is applied by a select, with no branch around the loads.
-template <int D>
+// Up to this many rows the merge takes D/32 warps a row (d = 128: 32 rows of 64
+// splits 5.7 -> 3.0 us, 256 of 32 splits 3.4 -> 2.1 us; 512 of 5 splits would
+// go from 2.2 to 2.5 us).
+constexpr int kCombineFewRows = 256;
+
+// One warp per (sequence, query head), or D/32 warps of it with one channel per
+// lane where the rows alone would leave multiprocessors idle (PER = 1). The
+// lanes read the split LSEs in parallel and reduce them with shuffles. The
+// partials are then streamed in batches of loads that are all issued before
+// the first is used, so a batch costs one L2 round trip: 16 of a float4 (d =
+// 128) or float2 (d = 64), or 32 of one float. The weight is applied by a
+// select, with no branch around the loads. Every channel is summed over the
+// splits in ascending order in both forms, so they give the same bits.
+template <int D, int PER>
 __global__ void __launch_bounds__(256) decode_combine_kernel(const float* __restrict__ o_part,
                                                              const float* __restrict__ lse_part, int n_split,
                                                              int rows, uint16_t* __restrict__ o,
                                                              float* __restrict__ lse_o) {
-  constexpr int PER = D / 32;  // d values per lane: 4 or 2
-  constexpr int BATCH = 16;
-  using VecT = typename std::conditional<PER == 4, float4, float2>::type;
+  constexpr int WPR = D / 32 / PER;  // warps per row
+  constexpr int BATCH = PER == 1 ? 32 : 16;
+  using VecT = typename std::conditional<PER == 4, float4, typename std::conditional<PER == 2, float2, float>::type>::type;
   griddep_wait();  // the partials come from the split kernel that precedes this one
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int w = blockIdx.x * 8 + (threadIdx.x >> 5), row = w / WPR;
   if (row >= rows) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, col = (w % WPR * 32 + lane) * PER;
   const float* lp = lse_part + size_t(row) * n_split;
   const float l0 = lane < n_split ? lp[lane] : -INFINITY;
   float mx = l0;
   for (int j = lane + 32; j < n_split; j += 32) mx = fmaxf(mx, lp[j]);
   mx = warp_max(mx);
   const float mref = (mx == -INFINITY) ? 0.f : mx;  // all splits empty: every weight is 0
-  const float* op = o_part + size_t(row) * n_split * D + lane * PER;
+  const float* op = o_part + size_t(row) * n_split * D + col;
   float acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -666,10 +674,10 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const float* __rest
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
         const float w0 = __shfl_sync(0xffffffffu, wl, (u0 + u) & 31);
-        const float w = (u0 + u < nj && w0 > 0.f) ? w0 : 0.f;
+        const float wt = (u0 + u < nj && w0 > 0.f) ? w0 : 0.f;
         const float* xv = reinterpret_cast<const float*>(&x[u]);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = w > 0.f ? fmaf(w, xv[e], acc[e]) : acc[e];
+        for (int e = 0; e < PER; ++e) acc[e] = wt > 0.f ? fmaf(wt, xv[e], acc[e]) : acc[e];
       }
     }
   }
@@ -677,14 +685,16 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const float* __rest
   const float inv = den == 0.f ? 0.f : 1.f / den;  // a partial whose LSE is NaN makes its row NaN
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] *= inv;
-  uint16_t* dst = o + size_t(row) * D + lane * PER;
+  uint16_t* dst = o + size_t(row) * D + col;
   if (PER == 4) {
     *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[PER > 2 ? 2 : 0], acc[PER > 3 ? 3 : 0]));
+        make_uint2(pack_bf16x2(acc[0], acc[PER > 1 ? 1 : 0]), pack_bf16x2(acc[PER > 2 ? 2 : 0], acc[PER > 3 ? 3 : 0]));
+  } else if (PER == 2) {
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[PER > 1 ? 1 : 0]);
   } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+    *dst = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
   }
-  if (lse_o != nullptr && lane == 0) lse_o[row] = den == 0.f ? -INFINITY : mx + logf(den);
+  if (lse_o != nullptr && lane == 0 && w % WPR == 0) lse_o[row] = den == 0.f ? -INFINITY : mx + logf(den);
 }
 
 template <int D, int G>
@@ -849,13 +859,20 @@ cudaError_t launch_decode_fused(const Shape& sh, const uint16_t* q, const uint16
   return sh.d == 128 ? launch_decode_fused_d<128>(sh, a, st) : launch_decode_fused_d<64>(sh, a, st);
 }
 
+template <int D, int PER>
+static cudaError_t launch_combine(int rows, int n_split, const float* o_part, const float* lse_part, uint16_t* o,
+                                  float* lse_o, cudaStream_t st) {
+  const int warps = rows * (D / 32 / PER);
+  return launch_pdl(decode_combine_kernel<D, PER>, dim3((warps + 7) / 8), dim3(256), 0, st, o_part, lse_part, n_split,
+                    rows, o, lse_o);
+}
+
 cudaError_t launch_decode_combine(const Shape& sh, int n_split, const float* o_part, const float* lse_part,
                                   uint16_t* o, float* lse_o, cudaStream_t st) {
   const int rows = sh.B * sh.Hq;
-  const dim3 grid((rows + 7) / 8), block(256);
-  const cudaError_t e =
-      sh.d == 128 ? launch_pdl(decode_combine_kernel<128>, grid, block, 0, st, o_part, lse_part, n_split, rows, o, lse_o)
-                  : launch_pdl(decode_combine_kernel<64>, grid, block, 0, st, o_part, lse_part, n_split, rows, o, lse_o);
+  const bool few = rows <= kCombineFewRows;
+  const cudaError_t e = sh.d == 128 ? (few ? launch_combine<128, 1> : launch_combine<128, 4>)(rows, n_split, o_part, lse_part, o, lse_o, st)
+                                    : (few ? launch_combine<64, 1> : launch_combine<64, 2>)(rows, n_split, o_part, lse_part, o, lse_o, st);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

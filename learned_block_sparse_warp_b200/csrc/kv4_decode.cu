@@ -37,12 +37,9 @@ using namespace kv4;
 
 namespace {
 
-constexpr int kWarps = dec::kThreads / 32;
-#ifndef KV4_OCC
-#define KV4_OCC 3
-#define KV4_SLOTS 3
-#endif
-constexpr int kSlots = KV4_SLOTS;           // record slots of a warp's ring
+constexpr int kWarps = dec::kThreads / 32;  // warps of a fused CTA
+constexpr int kSplitWarps = 4;              // warps of a split CTA
+constexpr int kSlots = 2;                   // record slots of a warp's ring
 constexpr int kMaxTasks = 256;      // blocks of one CTA's list (fused: the whole list of a row)
 constexpr float kPShift = 8.f;      // P is kept times 2^8
 constexpr int kStepField = 17;      // exponent field that the largest step gets in fp16 when the base is set
@@ -68,7 +65,7 @@ struct Kv4DecodeArgs {
 
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -76,15 +73,21 @@ __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint
 }
 __device__ __forceinline__ void mma_f16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ void mma_bf16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -260,9 +263,8 @@ __device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& 
     const Words<NG> w0 = lds_words<NG>(tile + F::k_word(g, t, 0)), w1 = lds_words<NG>(tile + F::k_word(g + 8, t, 0));
     const Words<NG / 2> s0 = lds_params<NG>(tile + F::k_step(g, 0)), s1 = lds_params<NG>(tile + F::k_step(g + 8, 0));
     const Words<NG / 2> m0 = lds_params<NG>(tile + F::min_at(g, 0)), m1 = lds_params<NG>(tile + F::min_at(g + 8, 0));
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t am[4] = {m0.w[0], m1.w[0], NG == 4 ? m0.w[NG / 2 - 1] : 0u, NG == 4 ? m1.w[NG / 2 - 1] : 0u};
-    mma_bf16_16816(x, am, q.sum[0], q.sum[1]);
+    float x[4];
+    mma_bf16_zero(x, m0.w[0], m1.w[0], NG == 4 ? m0.w[NG / 2 - 1] : 0u, NG == 4 ? m1.w[NG / 2 - 1] : 0u, q.sum[0], q.sum[1]);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       float c[4];
@@ -374,7 +376,7 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
     }
     uint32_t mx = st.lim;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) mx = __vmaxu2(mx, __vmaxu2(stp[j][0], stp[j][1]));
+    for (int j = 0; j < NG; ++j) mx = __vimax3_u16x2(mx, stp[j][0], stp[j][1]);
     if (__any_sync(0xffffffffu, mx != st.lim)) {  // a step past the limit, or the first that is not 0: the base moves up
       const uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
       const int old = int((st.lo & 0xffffu) >> 7), now = max(old, int(top >> 7) - kStepField);
@@ -424,17 +426,17 @@ __device__ __forceinline__ void ring_issue(uint8_t* ring, const Cache& c, int it
   }
 }
 
-// Runs a warp over blocks first, first + kWarps, ... < n of its CTA's list
+// Runs a warp over blocks first, first + W, ... < n of its CTA's list
 // (records rec_s, -1 for a block that is left out; gates lam_s). The item
 // numbered `issued` is the first that is not yet under way.
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
                                            const int* rec_s, const float* lam_s, int first, int n, int cur_at,
                                            int cur_ntok, int issued) {
-  const int mine = n > first ? (n - 1 - first) / kWarps + 1 : 0;
+  const int mine = n > first ? (n - 1 - first) / W + 1 : 0;
   auto issue = [&](int item, int slot) {
     if (item < 2 * mine) {
-      const int at = first + (item >> 1) * kWarps;
+      const int at = first + (item >> 1) * W;
       const int rec = rec_s[at];
       if (rec >= 0) ring_issue<D>(ring, a.c, item, slot, rec, at == cur_at ? cur_ntok : kBlock);
     }
@@ -446,7 +448,7 @@ __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st,
     slot = slot + 1 == kSlots ? 0 : slot + 1;
   };
   for (int i = 0; i < mine; ++i) {
-    const int at = first + i * kWarps;
+    const int at = first + i * W;
     const int ntok = rec_s[at] < 0 ? 0 : at == cur_at ? cur_ntok : kBlock;
     const float lam = lam_s[at];
     float2 S[kTiles][2];
@@ -548,23 +550,28 @@ __device__ __forceinline__ float lse_of(float M, float den) {
   return den == 0.f ? -INFINITY : (M + log2f(den) - kPShift) * kLn2;
 }
 
-template <int D>
+// Dynamic shared memory of a CTA of W warps: the rings, and the partials in their place.
+template <int D, int W>
 constexpr int smem_bytes() {
-  constexpr int ring = kWarps * kSlots * Fmt<D>::kRecord, part = kWarps * int(sizeof(Partial<D>));
+  constexpr int ring = W * kSlots * Fmt<D>::kRecord, part = W * int(sizeof(Partial<D>));
   return ring > part ? ring : part;
 }
 
 }  // namespace
 
-// One CTA per (sequence, KV head, split).
-template <int D>
-__global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_split_kernel(Kv4DecodeArgs a) {
+// One CTA per (sequence, KV head, split), or a cluster of CS (CLUSTER) whose
+// CTAs take every CS-th block of the split's run.
+template <int D, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kSplitWarps, 16 / kSplitWarps) kv4_decode_split_kernel(Kv4DecodeArgs a) {
   using F = Fmt<D>;
+  constexpr int W = kSplitWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int rec_s[kMaxDecodeBlocksPerSplit];
   __shared__ float lam_s[kMaxDecodeBlocksPerSplit];
+  const int CS = CLUSTER ? int(cg::this_cluster().num_blocks()) : 1;
+  const int rank = CLUSTER ? int(cg::this_cluster().block_rank()) : 0;
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int split = blockIdx.x % a.n_split, bh = blockIdx.x / a.n_split, b = bh / a.Hkv, h = bh % a.Hkv;
+  const int item = blockIdx.x / CS, split = item % a.n_split, bh = item / a.n_split, b = bh / a.Hkv, h = bh % a.Hkv;
   const int NB = a.Lmax / kBlock;
   uint8_t* ring = smem + warp * kSlots * F::kRecord;
   griddep_launch_dependents();  // the merge kernel may begin its launch; it waits for this grid's writes
@@ -577,8 +584,9 @@ __global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_split_kerne
   const int c = (L - 1) / kBlock, nl = 1 + min(a.K, c);
   const int per = (nl + a.n_split - 1) / a.n_split;
   const int lo = min(split * per, nl), n = min(lo + per, nl) - lo;
-  if (tid < n) {
-    const int pos = lo + tid;
+  const int nt = rank < n ? (n - 1 - rank) / CS + 1 : 0;
+  if (tid < nt) {
+    const int pos = lo + tid * CS + rank;
     int m = c;
     float lam = 0.f;
     if (pos > 0) {
@@ -598,26 +606,32 @@ __global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_split_kerne
   State<D> st;
   st.clear();
   __syncthreads();
-  run_blocks<D>(a, st, q, ring, rec_s, lam_s, warp, n, lo == 0 ? 0 : -1, L - c * kBlock, 0);
+  run_blocks<D, W>(a, st, q, ring, rec_s, lam_s, warp, nt, lo == 0 && rank == 0 ? 0 : -1, L - c * kBlock, 0);
   __syncthreads();  // the rings are done with
   Partial<D>* part = reinterpret_cast<Partial<D>*>(smem);
   store_partial<D>(st, part + warp);
-  __syncthreads();
-  for (int e = tid; e < a.G * D / 2; e += dec::kThreads) {
+  if (CLUSTER)
+    cg::this_cluster().sync();  // every partial of the cluster is in place
+  else
+    __syncthreads();
+  for (int e = rank * 32 * W + tid; e < a.G * D / 2; e += CS * 32 * W) {
     const int g = 2 * e / D, col = 2 * e % D;
     float2 o;
     float M;
-    const float den = merge_partials<D>([&](int r) { return part + r; }, kWarps, g, col, o, M);
+    const float den = merge_partials<D>(
+        [&](int r) { return CLUSTER ? cg::this_cluster().map_shared_rank(part, r / W) + r % W : part + r; }, CS * W, g,
+        col, o, M);
     const size_t row = (size_t(bh) * a.G + g) * a.n_split + split;
     *reinterpret_cast<float2*>(a.o_part + row * D + col) = o;
     if (col == 0) a.lse_part[row] = lse_of(M, den);
   }
+  if (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still read its partials
 }
 
 // One cluster per (sequence, KV head): each CTA selects the row's blocks
 // itself and takes every CS-th one.
 template <int D>
-__global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
+__global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
   using F = Fmt<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int sel_s[dec::kFusedMaxK];
@@ -632,7 +646,7 @@ __global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_fused_kerne
   const int NB = a.Lmax / kBlock;
   uint8_t* ring = smem + warp * kSlots * F::kRecord;
   // the keys lie in the rings of warps 1 to 3, behind warp 0's, which starts on the current block at once
-  static_assert((kWarps - 1) * kSlots * F::kRecord >= dec::kFusedMaxNB * 4 + 768 * 4, "keys, histogram, picks and candidates");
+  static_assert((kWarps - 1) * kSlots * F::kRecord >= dec::kFusedMaxNB * 4 + 768 * 4, "keys, histogram, picks, candidates");
   uint32_t* key_s = reinterpret_cast<uint32_t*>(smem + kSlots * F::kRecord);
   int* hist_s = reinterpret_cast<int*>(key_s + dec::kFusedMaxNB);
   int* app_s = hist_s + 256;
@@ -740,7 +754,7 @@ __global__ void __launch_bounds__(dec::kThreads, KV4_OCC) kv4_decode_fused_kerne
   __syncthreads();  // the tasks are placed, and the keys' rings are free
   State<D> st;
   st.clear();
-  run_blocks<D>(a, st, q, ring, rec_s, lam_s, warp, nt, rank == 0 ? 0 : -1, L - c * kBlock, issued);
+  run_blocks<D, kWarps>(a, st, q, ring, rec_s, lam_s, warp, nt, rank == 0 ? 0 : -1, L - c * kBlock, issued);
   __syncthreads();  // the rings are done with
   Partial<D>* part = reinterpret_cast<Partial<D>*>(smem);
   store_partial<D>(st, part + warp);
@@ -778,12 +792,48 @@ static Kv4DecodeArgs kv4_decode_args(const Shape& sh, const uint16_t* q, const C
   return a;
 }
 
+// Launches `kern` on `items` clusters of cs CTAs, as a dependent launch.
+static cudaError_t launch_clusters(void (*kern)(Kv4DecodeArgs), int items, int cs, int threads, int smem, cudaStream_t st,
+                                   const Kv4DecodeArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(items) * cs);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+static cudaError_t multiprocessors(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// Split form. The cluster size: the largest power of two that keeps every CTA
+// resident at once (16 warps per SM), at most 8 and at most half the blocks of
+// a split.
 template <int D>
 static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
-  auto kern = kv4_decode_split_kernel<D>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+  constexpr int W = kSplitWarps, smem = smem_bytes<D, W>();
+  static_assert(smem <= 48 * 1024, "no opt-in needed");
+  int sms = 0;
+  const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(unsigned(a.B) * a.Hkv * a.n_split), dim3(dec::kThreads), smem_bytes<D>(), st, a);
+  const int items = a.B * a.Hkv * a.n_split, per = (a.K + a.n_split) / a.n_split;
+  const int want = min(min(dec::kMaxCluster, (per + W - 1) / W), sms * (16 / W) / items);
+  int cs = 1;
+  while (cs * 2 <= want) cs *= 2;
+  if (cs == 1) return launch_pdl(kv4_decode_split_kernel<D, false>, dim3(items), dim3(32 * W), smem, st, a);
+  return launch_clusters(kv4_decode_split_kernel<D, true>, items, cs, 32 * W, smem, st, a);
 }
 
 cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl, const float* s,
@@ -803,31 +853,14 @@ cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c
 // resident CTAs, at most 8 and at most one per block of the list.
 template <int D>
 static cudaError_t launch_fused(const Kv4DecodeArgs& a, cudaStream_t st) {
-  auto kern = kv4_decode_fused_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+  constexpr int smem = smem_bytes<D, kWarps>();
+  static_assert(smem <= 48 * 1024, "no opt-in needed");
+  int sms = 0;
+  const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0, per_sm = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, dec::kThreads, smem_bytes<D>())) != cudaSuccess)
-    return e;
   const int rows = a.B * a.Hkv;
-  const int cs = max(1, min(min(dec::kMaxCluster, a.K + 1), sms * max(1, per_sm) / rows));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(rows) * cs);
-  cfg.blockDim = dim3(dec::kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<D>();
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  const int cs = max(1, min(min(dec::kMaxCluster, a.K + 1), sms * 3 / rows));
+  return launch_clusters(kv4_decode_fused_kernel<D>, rows, cs, dec::kThreads, smem, st, a);
 }
 
 cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl,
