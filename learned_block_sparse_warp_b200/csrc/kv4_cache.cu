@@ -9,6 +9,11 @@
 // that reach it become NaN.
 //
 // Read: bf16(s·code + m), one rounding. Means: (1/64) Σ (s·code + m) in fp32.
+//
+// All three are bound by the bytes they move. Write and read give a tile of 16
+// tokens to a warp, the means a record: enough independent 16-byte loads per
+// lane that the few dependent ones before them (length, page) are hidden by the
+// other warps of the multiprocessor.
 #include "kv4.cuh"
 
 namespace sas {
@@ -29,9 +34,33 @@ struct Quant8 {
   uint16_t s, m;   // bf16
 };
 
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
+
 // Four consecutive lanes hold a group, 8 bf16 channels each. Every lane of the
 // warp takes part.
+//
+// The quotient (x − m)/s is formed as (x − m)·r with r = 1/s raised by 2^-20,
+// which outweighs the reciprocal's error: a value half-way between two levels
+// goes up, as in the definition. fma adds 1.5·2^23, so the code is in the low
+// bits, rounded once. A value just under half-way may have gone up with them:
+// its residue x − m − s·code is below −s/2, and such a code is taken down.
 __device__ __forceinline__ Quant8 quantise8(const uint4& x) {
+  constexpr float kMagic = 12582912.f;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   __nv_bfloat162 mx = *reinterpret_cast<const __nv_bfloat162*>(&w[0]), mn = mx;
 #pragma unroll
@@ -50,65 +79,146 @@ __device__ __forceinline__ Quant8 quantise8(const uint4& x) {
   const float hi = __bfloat162float(e.x), lo = -__bfloat162float(e.y);
   const float range = __fsub_rn(hi, lo);
   const bool bad = !(fabsf(range) <= 3.402823466e38f);
-  __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
+  // range / 15, correctly rounded: one Newton correction is exact while the
+  // residue is a normal number
+  float quot = __fmul_rn(range, 0.0666666701436042785644531f);
+  quot = fmaf(fmaf(-15.f, quot, range), 0.0666666701436042785644531f, quot);
+  if (range < 1e-25f) quot = __fdiv_rn(range, 15.f);
+  __nv_bfloat16 sb = __float2bfloat16_rn(quot);
   float s = __bfloat162float(sb);
   if (bad || s < kMinStep) {
     s = 0.f;
     sb = __float2bfloat16_rn(0.f);
   }
-  // 1/s raised by 2^-20, which outweighs its rounding: a value half-way
-  // between two levels goes up, as in the definition. fma adds 1.5·2^23, so
-  // the code is in the low bits, rounded once.
-  const float inv = s > 0.f ? __fmul_rn(__fdiv_rn(1.f, s), 1.00000095367431640625f) : 0.f;
+  float r;
+  asm("rcp.approx.f32 %0, %1;\n" : "=f"(r) : "f"(s));
+  r = s > 0.f ? __fmul_rn(r, 1.00000095367431640625f) : 0.f;
+  float2 d[4], c[4];
+  float least = 0.f;
   uint32_t word = 0;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
-    const uint32_t cb = __float_as_uint(fmaf(__fsub_rn(b, lo), inv, 12582912.f));
-    const uint32_t ca = __float_as_uint(fmaf(__fsub_rn(a, lo), inv, 12582912.f));
-    word = (word << 8) | ((cb & 15u) << 4) | (ca & 15u);
+    d[i] = add_f32x2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), dup2(-lo));
+    c[i] = fma_f32x2(d[i], dup2(r), dup2(kMagic));
+    const float2 v = add_f32x2(c[i], dup2(-kMagic));
+    const float2 rest = fma_f32x2(v, dup2(-s), d[i]);
+    least = fminf(least, fminf(rest.x, rest.y));
+    word = word * 16u + __float_as_uint(c[i].y);
+    word = word * 16u + __float_as_uint(c[i].x);
   }
+  word -= 0x3f400000u;  // what the eight 1.5·2^23 leave in it
   Quant8 q;
-  q.word = bad ? 0u : word;
+  q.word = word;
+  if (least < -0.5f * s) {
+    word = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const float2 v = add_f32x2(c[i], dup2(-kMagic));
+      const uint32_t cb = uint32_t(v.y) - (fmaf(v.y, -s, d[i].y) < -0.5f * s ? 1u : 0u);
+      const uint32_t ca = uint32_t(v.x) - (fmaf(v.x, -s, d[i].x) < -0.5f * s ? 1u : 0u);
+      word = (word << 8) | (cb << 4) | ca;
+    }
+    q.word = word;
+  }
+  if (bad) q.word = 0u;
   q.s = __bfloat16_as_ushort(sb);
   q.m = bad ? uint16_t(0x7fc0u) : __bfloat16_as_ushort(__float2bfloat16_rn(__fadd_rn(lo, 0.f)));  // −0 becomes +0
   return q;
 }
 
-// D/8 lanes per token and KV head; blockIdx.y is 0 for K and 1 for V.
+// The tile of a warp: block m of sequence b and head h, and which of its 16
+// tokens [r0, r1) are new. i0 is the row of k and v that token 0 of the tile
+// would have.
+struct Tile {
+  int b, h, m, in_block, r0, r1, i0;
+};
+
+// Warp `item` of [bh][tile]. False where the window has no such tile.
+__device__ __forceinline__ bool tile_of(const Kv4Args& a, unsigned item, unsigned per, Tile* t) {
+  const unsigned bh = item / per;
+  if (bh >= unsigned(a.B) * a.Hkv) return false;
+  t->b = int(bh / a.Hkv);
+  t->h = int(bh % a.Hkv);
+  const Window w = window_of(a.cache_len, a.new_len, t->b, a.n_tokens, a.Lmax, a.err);
+  const int tile = w.pos / kTile + int(item % per), first = tile * kTile;
+  t->m = tile / kTiles;
+  t->in_block = tile % kTiles;
+  t->i0 = first - w.pos;
+  t->r0 = max(-t->i0, 0);
+  t->r1 = min(w.n - t->i0, kTile);
+  return t->r0 < t->r1;
+}
+
+// 16-byte unit of a V tile's codes in the staging buffer: unit (u, g, t) holds
+// the groups of one token pair. The order keeps the stores of one token pair in
+// different banks.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Args a, const uint16_t* __restrict__ k,
+__device__ __forceinline__ int stage_unit(int unit) {
+  return D == 128 && unit < 64 ? unit ^ ((unit >> 3) & 3) : unit;
+}
+
+// A warp per tile; blockIdx.y is 0 for K and 1 for V. D/8 lanes hold a token.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Args a, unsigned per, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v) {
   using F = Fmt<D>;
-  constexpr int LPR = D / 8;
+  constexpr int LPR = D / 8, TPI = 32 / LPR, NI = kTile / TPI;
+  __shared__ __align__(16) uint8_t stage_s[8][F::kTileBytes];
   griddep_launch_dependents();
   griddep_wait();
-  const int NB = a.Lmax / kBlock;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.y != 0;
-  const uint16_t* src = is_v ? v : k;
-  uint8_t* dst = is_v ? a.c.v : a.c.k;
-  const int l = threadIdx.x % LPR, j = l >> 2, q = l & 3;
-  const int64_t rows = int64_t(a.B) * a.Hkv * a.n_tokens;
-  for (int64_t r0 = int64_t(blockIdx.x) * (256 / LPR); r0 < rows; r0 += int64_t(gridDim.x) * (256 / LPR)) {
-    const int64_t row = r0 + threadIdx.x / LPR;
-    bool live = row < rows;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    int b = 0, h = 0, pos = 0;
-    if (live) {
-      const int i = int(row % a.n_tokens), bh = int(row / a.n_tokens);
-      b = bh / a.Hkv;
-      h = bh % a.Hkv;
-      const Window w = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
-      live = i < w.n;
-      pos = w.pos + i;
-      if (live) x = *reinterpret_cast<const uint4*>(src + row * D + 8 * l);
+  Tile t;
+  if (!tile_of(a, blockIdx.x * 8 + warp, per, &t)) return;
+  const int l = lane % LPR, j = l >> 2, q = l & 3;
+  const uint16_t* src = (is_v ? v : k) + (int64_t(t.b * a.Hkv + t.h) * a.n_tokens + t.i0) * D + 8 * l;
+  uint4 x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * TPI + lane / LPR;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r >= t.r0 && r < t.r1) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D));
+  }
+  const int rec = record_of(a.c, t.b, t.h, t.m, a.Hkv, a.Lmax / kBlock, a.err);
+  if (rec < 0) return;
+  uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + t.in_block * F::kTileBytes;
+  if (t.r1 - t.r0 == kTile) {  // the whole tile: staged, so that it leaves in 16-byte stores
+    uint8_t* stage = stage_s[warp];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * TPI + lane / LPR;
+      const Quant8 g = quantise8(x[i]);
+      if (is_v) {  // a word holds two tokens: the even one's lane takes the lower channels, the odd one's the upper
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, g.word, LPR);
+        const uint32_t w = (r & 1) ? __byte_perm(other, g.word, 0x7632) : __byte_perm(g.word, other, 0x5410);
+        const int at = F::v_half(r & ~1, 2 * q + (r & 1), j);
+        *reinterpret_cast<uint32_t*>(stage + stage_unit<D>(at >> 4) * 16 + (at & 15)) = w;
+      } else {
+        *reinterpret_cast<uint32_t*>(stage + F::k_word(r, q, j)) = g.word;
+      }
+      if (q == 0) {
+        *reinterpret_cast<uint16_t*>(stage + (is_v ? F::v_step(r, j) : F::k_step(r, j))) = g.s;
+        *reinterpret_cast<uint16_t*>(stage + F::min_at(r, j)) = g.m;
+      }
     }
-    const Quant8 g = quantise8(x);
-    if (!live) continue;
-    const int rec = record_of(a.c, b, h, pos / kBlock, a.Hkv, NB, a.err);
-    if (rec < 0) continue;
-    uint8_t* tile = dst + size_t(rec) * F::kRecord + (pos % kBlock) / kTile * F::kTileBytes;
-    const int r = pos % kTile;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < (F::kTileBytes + 511) / 512; ++i) {
+      const int unit = i * 32 + lane;
+      if (unit < F::kTileBytes / 16)
+        *reinterpret_cast<uint4*>(tile + unit * 16) =
+            *reinterpret_cast<const uint4*>(stage + (is_v ? stage_unit<D>(unit) : unit) * 16);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int i = t.r0 / TPI; i * TPI < t.r1; ++i) {  // a part of the tile: the other tokens' bits stay as they are
+    const int r = i * TPI + lane / LPR;
+    uint4 y = x[0];
+#pragma unroll
+    for (int u = 1; u < NI; ++u) y = u == i ? x[u] : y;
+    const Quant8 g = quantise8(y);
+    if (r < t.r0 || r >= t.r1) continue;
     if (is_v) {
       *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q, j)) = uint16_t(g.word);
       *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q + 1, j)) = uint16_t(g.word >> 16);
@@ -122,91 +232,178 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Args a, const uint16_
   }
 }
 
-// 8 values s·code + m of one word.
-__device__ __forceinline__ void values8(uint32_t word, float s, float m, float* x) {
+// Four registers (nibbles i and i + 4 of a word) as bf16 s·code + m: 128 + code
+// is the bf16 with the code in its low bits, 128 comes off exactly, and the fma
+// rounds once.
+__device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t m2, uint32_t (&r)[4]) {
+  const uint32_t base = 0x43004300u;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) x[p] = fmaf(s, __uint_as_float(0x4b000000u | ((word >> (4 * p)) & 15u)) - 8388608.f, m);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((word >> (4 * i)) & 0x000f000fu) | base;
+    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&base));
+    const __nv_bfloat162 y = __hfma2(n, *reinterpret_cast<const __nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&m2));
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 
+// N 32-bit words from a pointer aligned to all of them.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x, w[N > 1 ? 1 : 0] = x.y, w[N > 2 ? 2 : 0] = x.z, w[N > 3 ? 3 : 0] = x.w;
+  } else if (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[N > 1 ? 1 : 0] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// A warp per tile; blockIdx.y is 0 for K and 1 for V. A lane reads the words of
+// one (token, t) of K or (g, token pair) of V and writes 16 or 2 x 8 bytes per
+// group, so that four or eight lanes fill 64 bytes of an output row.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Args a, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
+__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Args a, unsigned per, uint16_t* __restrict__ k,
+                                                       uint16_t* __restrict__ v) {
   using F = Fmt<D>;
-  constexpr int LPR = D / 8;
+  constexpr int NG = F::NG;
   griddep_launch_dependents();
   griddep_wait();
-  const int NB = a.Lmax / kBlock;
+  const int lane = threadIdx.x & 31;
   const bool is_v = blockIdx.y != 0;
   uint16_t* dst = is_v ? v : k;
-  const uint8_t* src = is_v ? a.c.v : a.c.k;
   if (dst == nullptr) return;
-  const int l = threadIdx.x % LPR, j = l >> 2, q = l & 3;
-  const int64_t rows = int64_t(a.B) * a.Hkv * a.n_tokens;
-  for (int64_t row = int64_t(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR; row < rows;
-       row += int64_t(gridDim.x) * (256 / LPR)) {
-    const int i = int(row % a.n_tokens), bh = int(row / a.n_tokens);
-    const int b = bh / a.Hkv, h = bh % a.Hkv;
-    const Window w = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
-    if (i >= w.n) continue;
-    const int pos = w.pos + i;
-    const int rec = record_of(a.c, b, h, pos / kBlock, a.Hkv, NB, a.err);
-    if (rec < 0) continue;
-    const uint8_t* tile = src + size_t(rec) * F::kRecord + (pos % kBlock) / kTile * F::kTileBytes;
-    const int r = pos % kTile;
-    uint32_t word;
-    if (is_v)
-      word = uint32_t(*reinterpret_cast<const uint16_t*>(tile + F::v_half(r, 2 * q, j))) |
-             uint32_t(*reinterpret_cast<const uint16_t*>(tile + F::v_half(r, 2 * q + 1, j))) << 16;
-    else
-      word = *reinterpret_cast<const uint32_t*>(tile + F::k_word(r, q, j));
-    const float s = bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + (is_v ? F::v_step(r, j) : F::k_step(r, j))));
-    const float m = bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + F::min_at(r, j)));
-    float x[8];
-    values8(word, s, m, x);
-    *reinterpret_cast<uint4*>(dst + row * D + 8 * l) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  Tile tl;
+  if (!tile_of(a, blockIdx.x * 8 + (threadIdx.x >> 5), per, &tl)) return;
+  const int rec = record_of(a.c, tl.b, tl.h, tl.m, a.Hkv, a.Lmax / kBlock, a.err);
+  if (rec < 0) return;
+  const uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + tl.in_block * F::kTileBytes;
+  dst += (int64_t(tl.b * a.Hkv + tl.h) * a.n_tokens + tl.i0) * D;
+  const int g = lane >> 2, t = lane & 3;
+  if (is_v) {
+    uint32_t w[2][NG], s[2 * NG], m[2][2][NG / 2];  // s: groups x token pairs; m: [pair][token of it]
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load_words<NG>(tile + F::v_half(8 * u + 2 * t, g, 0), w[u]);
+      load_words<NG / 2>(tile + F::min_at(8 * u + 2 * t, 0), m[u][0]);
+      load_words<NG / 2>(tile + F::min_at(8 * u + 2 * t + 1, 0), m[u][1]);
+    }
+#pragma unroll
+    for (int j = 0; j < NG; j += 2) {
+      const uint4 y = *reinterpret_cast<const uint4*>(tile + F::kSteps + (t * NG + j) * 8);
+      s[2 * j] = y.x, s[2 * j + 1] = y.y, s[2 * j + 2] = y.z, s[2 * j + 3] = y.w;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = 8 * u + 2 * t;
+      const bool even = r >= tl.r0 && r < tl.r1, odd = r + 1 >= tl.r0 && r + 1 < tl.r1;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        uint32_t y[4];
+        dequant8(w[u][j], s[2 * j + u], __byte_perm(m[u][0][j / 2], m[u][1][j / 2], (j & 1) ? 0x7632 : 0x5410), y);
+        uint16_t* o = dst + r * D + 32 * j + 4 * g;
+        if (even) __stcs(reinterpret_cast<uint2*>(o), make_uint2(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410)));
+        if (odd) __stcs(reinterpret_cast<uint2*>(o + D), make_uint2(__byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
+      }
+    }
+  } else {
+    uint32_t w[2][NG], s[2][NG / 2], m[2][NG / 2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load_words<NG>(tile + F::k_word(8 * u + g, t, 0), w[u]);
+      load_words<NG / 2>(tile + F::k_step(8 * u + g, 0), s[u]);
+      load_words<NG / 2>(tile + F::min_at(8 * u + g, 0), m[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = 8 * u + g;
+      const bool live = r >= tl.r0 && r < tl.r1;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const uint32_t sel = (j & 1) ? 0x3232 : 0x1010;
+        uint32_t y[4];
+        dequant8(w[u][j], __byte_perm(s[u][j / 2], 0, sel), __byte_perm(m[u][j / 2], 0, sel), y);
+        if (live)
+          __stcs(reinterpret_cast<uint4*>(dst + r * D + 32 * j + 8 * t),
+                 make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                            __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
+      }
+    }
   }
 }
 
-// One warp per (sequence, KV head, candidate block). D/8 lanes cover a token's
-// words, so 32/(D/8) tokens are summed side by side.
+// One warp per (sequence, KV head, candidate block). A lane sums the 8 tokens
+// g, g + 8, ... of its t, 8 channels per group; the lanes of a t are then added
+// pairwise, each keeping half of the channels.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_means_kernel(Kv4Args a, uint16_t* __restrict__ kmean) {
+__global__ void __launch_bounds__(128) kv4_means_kernel(Kv4Args a, unsigned per, uint16_t* __restrict__ kmean) {
   using F = Fmt<D>;
-  constexpr int LPR = D / 8, TP = 32 / LPR;
+  constexpr int NG = F::NG;
   griddep_launch_dependents();
   griddep_wait();
   const int NB = a.Lmax / kBlock;
-  const int per = (a.n_tokens + kBlock - 1) / kBlock;  // most blocks that n_tokens tokens can complete
-  const int64_t items = int64_t(a.B) * a.Hkv * per;
-  const int lane = threadIdx.x & 31, l = lane % LPR, j = l >> 2, q = l & 3;
-  for (int64_t it = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += int64_t(gridDim.x) * 8) {
-    const int bh = int(it / per), b = bh / a.Hkv, h = bh % a.Hkv;
-    const Window w = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
-    const int m = w.pos / kBlock + int(it % per);
-    if (kBlock * (m + 1) > w.pos + w.n || w.n == 0) continue;
-    const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-    if (rec < 0) continue;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int tok = lane / LPR; tok < kBlock; tok += TP) {
-      const uint8_t* tile = a.c.k + size_t(rec) * F::kRecord + tok / kTile * F::kTileBytes;
-      const int r = tok % kTile;
-      float x[8];
-      values8(*reinterpret_cast<const uint32_t*>(tile + F::k_word(r, q, j)),
-              bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + F::k_step(r, j))),
-              bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + F::min_at(r, j))), x);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const unsigned item = blockIdx.x * 4 + (threadIdx.x >> 5), bh = item / per;
+  if (bh >= unsigned(a.B) * a.Hkv) return;
+  const int b = int(bh / a.Hkv), h = int(bh % a.Hkv);
+  const Window wd = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
+  const int m = wd.pos / kBlock + int(item % per);
+  if (wd.n == 0 || kBlock * (m + 1) > wd.pos + wd.n) return;
+  const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
+  if (rec < 0) return;
+  const uint8_t* base = a.c.k + size_t(rec) * F::kRecord;
+  uint32_t w[2 * kTiles][NG], s[2 * kTiles][NG / 2], lo[2 * kTiles][NG / 2];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) acc[p] += x[p];
-    }
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-#pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) acc[p] += __shfl_xor_sync(0xffffffffu, acc[p], o);
-      acc[p] *= 1.f / kBlock;
-    }
-    if (lane < LPR)
-      *reinterpret_cast<uint4*>(kmean + ((size_t(bh) * NB + m) * D + 8 * l)) = make_uint4(
-          pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+  for (int i = 0; i < 2 * kTiles; ++i) {
+    const uint8_t* tile = base + i / 2 * F::kTileBytes;
+    const int r = g + 8 * (i & 1);
+    load_words<NG>(tile + F::k_word(r, t, 0), w[i]);
+    load_words<NG / 2>(tile + F::k_step(r, 0), s[i]);
+    load_words<NG / 2>(tile + F::min_at(r, 0), lo[i]);
   }
+  float2 acc[NG][4];  // channels 32 j + 8 t + {2 i, 2 i + 1}
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    float low = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 2 * kTiles; ++i) {
+      const float sf = __uint_as_float((j & 1) ? s[i][j / 2] & 0xffff0000u : s[i][j / 2] << 16);
+      low += __uint_as_float((j & 1) ? lo[i][j / 2] & 0xffff0000u : lo[i][j / 2] << 16);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // 2^23 + code has the code in its low bits
+        const float2 n = add_f32x2(make_float2(__uint_as_float(0x4b000000u | ((w[i][j] >> (8 * c)) & 15u)),
+                                               __uint_as_float(0x4b000000u | ((w[i][j] >> (8 * c + 4)) & 15u))),
+                                   dup2(-8388608.f));
+        acc[j][c] = fma_f32x2(n, dup2(sf), acc[j][c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[j][c] = add_f32x2(acc[j][c], dup2(low));
+  }
+  // lanes g and g ^ 4 swap halves of the groups, then g ^ 2 and g ^ 1 halves of what is left
+  constexpr int N = NG * 8;
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) x[2 * i] = acc[i / 4][i % 4].x, x[2 * i + 1] = acc[i / 4][i % 4].y;
+#pragma unroll
+  for (int o = 16, n = N / 2; o >= 4; o >>= 1, n >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? x[i] : x[n + i], keep = up ? x[n + i] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  // this lane has the N/8 channels from N/8 · g of its t's list
+  uint16_t* out = kmean + (size_t(bh) * NB + m) * D;
+  const int c0 = g * (N / 8), ch = 32 * (c0 / 8) + 8 * t + c0 % 8;
+  if (NG == 4)
+    *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_bf16x2(x[0] / kBlock, x[1] / kBlock), pack_bf16x2(x[2] / kBlock, x[3] / kBlock));
+  else
+    *reinterpret_cast<uint32_t*>(out + ch) = pack_bf16x2(x[0] / kBlock, x[1] / kBlock);
 }
 
 static Kv4Args kv4_args(const Shape& sh, const Cache& c, int n_tokens, const int32_t* cache_len,
@@ -214,36 +411,41 @@ static Kv4Args kv4_args(const Shape& sh, const Cache& c, int n_tokens, const int
   return {c, cache_len, new_len, n_tokens, sh.B, sh.Hkv, sh.N, err};
 }
 
-static unsigned kv4_grid(int64_t items, int per_cta) {
-  const int64_t n = (items + per_cta - 1) / per_cta;
-  return unsigned(n < 1 ? 1 : n > (1 << 30) ? (1 << 30) : n);
+// The most 16-token tiles that n_tokens tokens can touch.
+static unsigned tiles_of(int n_tokens) { return unsigned(n_tokens + kTile - 2) / kTile + 1; }
+
+// CTAs of `warps` warps for `per` items of every sequence and head.
+static bool kv4_grid(const Shape& sh, unsigned per, int warps, unsigned* ctas) {
+  const uint64_t items = uint64_t(sh.B) * sh.Hkv * per;
+  *ctas = unsigned((items + warps - 1) / warps);
+  return items < (uint64_t(1) << 32) - 64;
 }
 
 cudaError_t launch_kv4_write(const Shape& sh, const Cache& c, int n_tokens, const uint16_t* k, const uint16_t* v,
                              const int32_t* cache_len, const int32_t* new_len, int* err, cudaStream_t st) {
   const Kv4Args a = kv4_args(sh, c, n_tokens, cache_len, new_len, err);
-  const dim3 grid(kv4_grid(int64_t(sh.B) * sh.Hkv * n_tokens, 256 / (sh.d / 8)), 2);
-  const cudaError_t e = sh.d == 128 ? launch_pdl(kv4_write_kernel<128>, grid, dim3(256), 0, st, a, k, v)
-                                    : launch_pdl(kv4_write_kernel<64>, grid, dim3(256), 0, st, a, k, v);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const unsigned per = tiles_of(n_tokens);
+  unsigned n;
+  if (!kv4_grid(sh, per, 8, &n)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(sh.d == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>, dim3(n, 2), dim3(256), 0, st, a, per, k, v);
 }
 
 cudaError_t launch_kv4_read(const Shape& sh, const Cache& c, int n_tokens, uint16_t* k, uint16_t* v,
                             const int32_t* cache_len, const int32_t* new_len, int* err, cudaStream_t st) {
   const Kv4Args a = kv4_args(sh, c, n_tokens, cache_len, new_len, err);
-  const dim3 grid(kv4_grid(int64_t(sh.B) * sh.Hkv * n_tokens, 256 / (sh.d / 8)), 2);
-  const cudaError_t e = sh.d == 128 ? launch_pdl(kv4_read_kernel<128>, grid, dim3(256), 0, st, a, k, v)
-                                    : launch_pdl(kv4_read_kernel<64>, grid, dim3(256), 0, st, a, k, v);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const unsigned per = tiles_of(n_tokens);
+  unsigned n;
+  if (!kv4_grid(sh, per, 8, &n)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(sh.d == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, dim3(n, 2), dim3(256), 0, st, a, per, k, v);
 }
 
 cudaError_t launch_kv4_means(const Shape& sh, const Cache& c, int n_tokens, const int32_t* cache_len,
                              const int32_t* new_len, uint16_t* kmean, int* err, cudaStream_t st) {
   const Kv4Args a = kv4_args(sh, c, n_tokens, cache_len, new_len, err);
-  const dim3 grid(kv4_grid(int64_t(sh.B) * sh.Hkv * ((n_tokens + kBlock - 1) / kBlock), 8));
-  const cudaError_t e = sh.d == 128 ? launch_pdl(kv4_means_kernel<128>, grid, dim3(256), 0, st, a, kmean)
-                                    : launch_pdl(kv4_means_kernel<64>, grid, dim3(256), 0, st, a, kmean);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const unsigned per = unsigned(n_tokens + kBlock - 1) / kBlock;  // the most blocks that n_tokens tokens can complete
+  unsigned n;
+  if (!kv4_grid(sh, per, 4, &n)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(sh.d == 128 ? kv4_means_kernel<128> : kv4_means_kernel<64>, dim3(n), dim3(128), 0, st, a, per, kmean);
 }
 
 }  // namespace sas
