@@ -173,8 +173,14 @@ def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None, shape=N
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a torch.cuda.Stream around it, which costs 3.3 us a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -440,9 +446,15 @@ def empty_kv4_cache(p: Params, n_pages: Optional[int] = None, block_table: Optio
                     torch.empty(shape, dtype=torch.uint8, device=device), block_table)
 
 
+def _tokens(t, name: str) -> int:
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [B, Hkv, T, d], got shape {tuple(t.shape)}")
+    return t.shape[2]
+
+
 def sas_kv4_write(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
     """Quantises k, v [B, Hkv, T, d] into the cache at positions cache_len - new_len .. cache_len - 1 (new_len: T)."""
-    c, dev, T = cache.of(p), cache.device, k.shape[2]
+    c, dev, T = cache.of(p), cache.device, _tokens(k, "k")
     sh = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_write", lib.sas_kv4_write(
         p.c(), c, T, _arg(k, bf16, sh, "k", dev), _arg(v, bf16, sh, "v", dev),
@@ -455,7 +467,7 @@ def sas_kv4_read(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stre
     c, dev = cache.of(p), cache.device
     if k is None and v is None:
         raise ValueError("k, v: at least one output is needed")
-    T = (v if k is None else k).shape[2]
+    T = _tokens(v, "v") if k is None else _tokens(k, "k")
     sh = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_read", lib.sas_kv4_read(
         p.c(), c, T, _opt(k, bf16, sh, "k", dev), _opt(v, bf16, sh, "v", dev),
@@ -597,12 +609,30 @@ def decode_step_scored(p: Params, q, kc, vc, kmean, cache_len, s, n_split: int, 
     sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
 
 
+def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream) -> None:
+    """Select, split-K attention and merge over a 4-bit cache, every argument checked once and before the first
+    launch. select(c, pointers..., stream) launches the selection."""
+    ref, dev, st = cache.of(p), cache.device, _stream(stream)
+    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+    qp, lp = _arg(q, bf16, (B, Hq, d), "q", dev), _arg(cache_len, i32, (B,), "cache_len", dev)
+    sp = _arg(s, f32, (B, Hkv, p.n_blocks), "s", dev)
+    ip = _arg(out["idx"], i32, (B, Hkv, p.top_k), "idx", dev)
+    ep = _arg(out["lse_s"], f32, (B, Hkv), "lse_s", dev)
+    op = _arg(out["o_part"], f32, (B, Hq, n_split, d), "o_part", dev)
+    xp = _arg(out["lse_part"], f32, (B, Hq, n_split), "lse_part", dev)
+    yp, zp = _arg(out["o"], bf16, (B, Hq, d), "o", dev), _opt(out.get("lse_o"), f32, (B, Hq), "lse_o", dev)
+    c = p.c()
+    select(c, qp, lp, sp, ip, ep, st)
+    _check("sas_decode_kv4", lib.sas_decode_kv4(c, qp, ref, lp, sp, ip, ep, n_split, op, xp, st))
+    _check("sas_decode_combine", lib.sas_decode_combine(c, n_split, op, xp, yp, zp, st))
+
+
 def decode_step_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, stream=None) -> None:
     """One decode step over a 4-bit cache: Top-K select (decode form), split-K attention, LSE merge."""
-    sas_topk_select(p, s, out["idx"], out["lse_s"], cache_len=cache_len, stream=stream)
-    sas_decode_kv4(p, q, cache, cache_len, s, out["idx"], out["lse_s"], n_split, out["o_part"], out["lse_part"],
-                   stream=stream)
-    sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
+    def select(c, qp, lp, sp, ip, ep, st):
+        _check("sas_topk_select", lib.sas_topk_select(c, sp, lp, ip, ep, st))
+
+    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream)
 
 
 def decode_step_fused_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, out: dict, stream=None) -> None:
@@ -617,12 +647,16 @@ def decode_step_scored_kv4(p: Params, q, k_new, v_new, cache: Kv4Cache, kmean, c
     """A whole serving step over a 4-bit cache that scores its own history: write the new token (k_new, v_new
     [B, Hkv, 1, d], at position cache_len - 1), update the block means of the blocks it completed, score and
     select in one launch (s is written), split-K attention, merge."""
-    sas_kv4_write(p, cache, k_new, v_new, cache_len, stream=stream)
-    sas_kv4_block_mean_keys(p, cache, 1, cache_len, kmean, stream=stream)
-    sas_decode_select_scored(p, q, kmean, cache_len, s, out["idx"], out["lse_s"], stream=stream)
-    sas_decode_kv4(p, q, cache, cache_len, s, out["idx"], out["lse_s"], n_split, out["o_part"], out["lse_part"],
-                   stream=stream)
-    sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
+    if _tokens(k_new, "k_new") != 1:
+        raise ValueError(f"k_new: expected one token, got {k_new.shape[2]}")
+    kp = _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", cache.device)
+
+    def select(c, qp, lp, sp, ip, ep, st):
+        sas_kv4_write(p, cache, k_new, v_new, cache_len, stream=stream)
+        sas_kv4_block_mean_keys(p, cache, 1, cache_len, kmean, stream=stream)
+        _check("sas_decode_select_scored", lib.sas_decode_select_scored(c, qp, kp, lp, sp, ip, ep, st))
+
+    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream)
 
 
 class DecodeGraph:
