@@ -28,10 +28,10 @@ struct Kv4Args {
   int* err;
 };
 
-// One group's parameters and this lane's 8 codes.
-struct Quant8 {
-  uint32_t word;   // nibble p: code of the lane's channel p
-  uint16_t s, m;   // bf16
+// One group's parameters and the codes of this lane's two 8-channel chunks.
+struct Quant16 {
+  uint32_t word[2];  // nibble p: code of the chunk's channel p
+  uint16_t s, m;     // bf16
 };
 
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
@@ -51,78 +51,88 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
 
-// Four consecutive lanes hold a group, 8 bf16 channels each. Every lane of the
-// warp takes part.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two neighbouring lanes hold a group, 16 bf16 channels each. Every lane of the
+// warp takes part. Sixteen channels a lane rather than eight, because the
+// group's parameters cost as much as eight of its codes, and the arithmetic is
+// what bounds a long write.
 //
 // The quotient (x − m)/s is formed as (x − m)·r with r = 1/s raised by 2^-20,
 // which outweighs the reciprocal's error: a value half-way between two levels
 // goes up, as in the definition. fma adds 1.5·2^23, so the code is in the low
 // bits, rounded once. A value just under half-way may have gone up with them:
 // its residue x − m − s·code is below −s/2, and such a code is taken down.
-__device__ __forceinline__ Quant8 quantise8(const uint4& x) {
+__device__ __forceinline__ Quant16 quantise16(const uint4 (&x)[2]) {
   constexpr float kMagic = 12582912.f;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
   __nv_bfloat162 mx = *reinterpret_cast<const __nv_bfloat162*>(&w[0]), mn = mx;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
+  for (int i = 1; i < 8; ++i) {
     const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
     mx = __hmax2_nan(mx, v);
     mn = __hmin2_nan(mn, v);
   }
   // (max, −min) in one register: one shuffle serves both
-  __nv_bfloat162 e = __halves2bfloat162(__hmax_nan(mx.x, mx.y), __hneg(__hmin_nan(mn.x, mn.y)));
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    const uint32_t u = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&e), o);
-    e = __hmax2_nan(e, *reinterpret_cast<const __nv_bfloat162*>(&u));
-  }
-  const float hi = __bfloat162float(e.x), lo = -__bfloat162float(e.y);
-  const float range = __fsub_rn(hi, lo);
-  const bool bad = !(fabsf(range) <= 3.402823466e38f);
+  const uint32_t mxb = *reinterpret_cast<const uint32_t*>(&mx), mnb = *reinterpret_cast<const uint32_t*>(&mn) ^ 0x80008000u;
+  const uint32_t lo2 = __byte_perm(mxb, mnb, 0x5410), hi2 = __byte_perm(mxb, mnb, 0x7632);
+  __nv_bfloat162 e = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&lo2), *reinterpret_cast<const __nv_bfloat162*>(&hi2));
+  uint32_t eb = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&e), 1);
+  e = __hmax2_nan(e, *reinterpret_cast<const __nv_bfloat162*>(&eb));
+  eb = *reinterpret_cast<const uint32_t*>(&e);
+  const float hi = __uint_as_float(eb << 16), neg_lo = __uint_as_float(eb & 0xffff0000u);
+  const float range = __fadd_rn(hi, neg_lo);
+  const bool bad = !(range <= 3.402823466e38f);
   // range / 15, correctly rounded: one Newton correction is exact while the
   // residue is a normal number
   float quot = __fmul_rn(range, 0.0666666701436042785644531f);
   quot = fmaf(fmaf(-15.f, quot, range), 0.0666666701436042785644531f, quot);
   if (range < 1e-25f) quot = __fdiv_rn(range, 15.f);
-  __nv_bfloat16 sb = __float2bfloat16_rn(quot);
-  float s = __bfloat162float(sb);
-  if (bad || s < kMinStep) {
-    s = 0.f;
-    sb = __float2bfloat16_rn(0.f);
-  }
+  const uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(quot));
+  const bool flat = bad || sb < 0x80u;  // a step below 2^-126, or no range
+  const float s = flat ? 0.f : bf16_to_f32(sb);
   float r;
-  asm("rcp.approx.f32 %0, %1;\n" : "=f"(r) : "f"(s));
-  r = s > 0.f ? __fmul_rn(r, 1.00000095367431640625f) : 0.f;
-  float2 d[4], c[4];
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(s));
+  r = flat ? 0.f : __fmul_rn(r, 1.00000095367431640625f);
   float least = 0.f;
-  uint32_t word = 0;
+  Quant16 q;
 #pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    d[i] = add_f32x2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), dup2(-lo));
-    c[i] = fma_f32x2(d[i], dup2(r), dup2(kMagic));
-    const float2 v = add_f32x2(c[i], dup2(-kMagic));
-    const float2 rest = fma_f32x2(v, dup2(-s), d[i]);
-    least = fminf(least, fminf(rest.x, rest.y));
-    word = word * 16u + __float_as_uint(c[i].y);
-    word = word * 16u + __float_as_uint(c[i].x);
-  }
-  word -= 0x3f400000u;  // what the eight 1.5·2^23 leave in it
-  Quant8 q;
-  q.word = word;
-  if (least < -0.5f * s) {
-    word = 0;
+  for (int h = 0; h < 2; ++h) {
+    uint32_t word = 0;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      const float2 v = add_f32x2(c[i], dup2(-kMagic));
-      const uint32_t cb = uint32_t(v.y) - (fmaf(v.y, -s, d[i].y) < -0.5f * s ? 1u : 0u);
-      const uint32_t ca = uint32_t(v.x) - (fmaf(v.x, -s, d[i].x) < -0.5f * s ? 1u : 0u);
-      word = (word << 8) | (cb << 4) | ca;
+    for (int i = 4 * h + 3; i >= 4 * h; --i) {
+      const float2 d = add_f32x2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), dup2(neg_lo));
+      const float2 c = fma_f32x2(d, dup2(r), dup2(kMagic));
+      const float2 rest = fma_f32x2(add_f32x2(c, dup2(-kMagic)), dup2(-s), d);
+      least = min3(least, rest.x, rest.y);
+      word = word * 16u + __float_as_uint(c.y);
+      word = word * 16u + __float_as_uint(c.x);
     }
-    q.word = word;
+    q.word[h] = word - 0x3f400000u;  // less what the eight 1.5·2^23 leave in it
   }
-  if (bad) q.word = 0u;
-  q.s = __bfloat16_as_ushort(sb);
-  q.m = bad ? uint16_t(0x7fc0u) : __bfloat16_as_ushort(__float2bfloat16_rn(__fadd_rn(lo, 0.f)));  // −0 becomes +0
+  if (least < -0.5f * s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 4 * h + 3; i >= 4 * h; --i)
+#pragma unroll
+        for (int e = 1; e >= 0; --e) {
+          const float d = __fadd_rn(__uint_as_float(e ? w[i] & 0xffff0000u : w[i] << 16), neg_lo);
+          const float n = fmaf(d, r, kMagic) - kMagic;
+          word = (word << 4) | (uint32_t(n) - (fmaf(n, -s, d) < -0.5f * s ? 1u : 0u));
+        }
+      q.word[h] = word;
+    }
+  }
+  if (bad) q.word[0] = q.word[1] = 0u;
+  q.s = flat ? uint16_t(0) : sb;
+  const uint16_t mb = uint16_t(eb >> 16) ^ uint16_t(0x8000);
+  q.m = bad ? uint16_t(0x7fc0u) : mb == 0x8000u ? uint16_t(0) : mb;  // −0 becomes +0
   return q;
 }
 
@@ -157,78 +167,103 @@ __device__ __forceinline__ int stage_unit(int unit) {
   return D == 128 && unit < 64 ? unit ^ ((unit >> 3) & 3) : unit;
 }
 
-// A warp per tile; blockIdx.y is 0 for K and 1 for V. D/8 lanes hold a token.
+// Warps of a write CTA. The bound of 28 warps per multiprocessor (72 registers)
+// measures best: at the 91 registers of the unbounded kernel 32K tokens take 41
+// us, with it 30 us.
+constexpr int kWriteWarps = 4;
+
+// A token's codes, step and minimum to their places in a tile in global memory.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Args a, unsigned per, const uint16_t* __restrict__ k,
+__device__ __forceinline__ void store_token(uint8_t* tile, bool is_v, int r, int j, int hq, const Quant16& g) {
+  using F = Fmt<D>;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int q = hq + 2 * u;
+    if (is_v) {
+      *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q, j)) = uint16_t(g.word[u]);
+      *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q + 1, j)) = uint16_t(g.word[u] >> 16);
+    } else {
+      *reinterpret_cast<uint32_t*>(tile + F::k_word(r, q, j)) = g.word[u];
+    }
+  }
+  if (hq == 0) {
+    *reinterpret_cast<uint16_t*>(tile + (is_v ? F::v_step(r, j) : F::k_step(r, j))) = g.s;
+    *reinterpret_cast<uint16_t*>(tile + F::min_at(r, j)) = g.m;
+  }
+}
+
+// A warp per tile; blockIdx.y is 0 for K and 1 for V. D/16 lanes hold a token:
+// lane (j, hq) has the chunks hq and hq + 2 of group j's four, so that each
+// load fills 32-byte sectors.
+template <int D>
+__global__ void __launch_bounds__(32 * kWriteWarps, 28 / kWriteWarps) kv4_write_kernel(Kv4Args a, unsigned per, const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v) {
   using F = Fmt<D>;
-  constexpr int LPR = D / 8, TPI = 32 / LPR, NI = kTile / TPI;
-  __shared__ __align__(16) uint8_t stage_s[8][F::kTileBytes];
+  constexpr int LPR = D / 16, TPI = 32 / LPR, NI = kTile / TPI;
+  __shared__ __align__(16) uint8_t stage_s[kWriteWarps][F::kTileBytes];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_v = blockIdx.y != 0;
   Tile t;
-  if (!tile_of(a, blockIdx.x * 8 + warp, per, &t)) return;
-  const int l = lane % LPR, j = l >> 2, q = l & 3;
-  const uint16_t* src = (is_v ? v : k) + (int64_t(t.b * a.Hkv + t.h) * a.n_tokens + t.i0) * D + 8 * l;
-  uint4 x[NI];
+  if (!tile_of(a, blockIdx.x * (kWriteWarps) + warp, per, &t)) return;
+  const int j = lane % LPR >> 1, hq = lane & 1, at = lane / LPR;
+  const uint16_t* src = (is_v ? v : k) + (int64_t(t.b * a.Hkv + t.h) * a.n_tokens + t.i0) * D + 32 * j + 8 * hq;
+  uint4 x[NI][2];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int r = i * TPI + lane / LPR;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r >= t.r0 && r < t.r1) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D));
+    const int r = i * TPI + at;
+    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+    if (r >= t.r0 && r < t.r1) {
+      x[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D));
+      x[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D + 16));
+    }
   }
   const int rec = record_of(a.c, t.b, t.h, t.m, a.Hkv, a.Lmax / kBlock, a.err);
   if (rec < 0) return;
   uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + t.in_block * F::kTileBytes;
-  if (t.r1 - t.r0 == kTile) {  // the whole tile: staged, so that it leaves in 16-byte stores
-    uint8_t* stage = stage_s[warp];
+  if (t.r1 - t.r0 < kTile) {  // a part of the tile: the other tokens' bits stay as they are
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int r = i * TPI + lane / LPR;
-      const Quant8 g = quantise8(x[i]);
-      if (is_v) {  // a word holds two tokens: the even one's lane takes the lower channels, the odd one's the upper
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, g.word, LPR);
-        const uint32_t w = (r & 1) ? __byte_perm(other, g.word, 0x7632) : __byte_perm(g.word, other, 0x5410);
-        const int at = F::v_half(r & ~1, 2 * q + (r & 1), j);
-        *reinterpret_cast<uint32_t*>(stage + stage_unit<D>(at >> 4) * 16 + (at & 15)) = w;
-      } else {
-        *reinterpret_cast<uint32_t*>(stage + F::k_word(r, q, j)) = g.word;
-      }
-      if (q == 0) {
-        *reinterpret_cast<uint16_t*>(stage + (is_v ? F::v_step(r, j) : F::k_step(r, j))) = g.s;
-        *reinterpret_cast<uint16_t*>(stage + F::min_at(r, j)) = g.m;
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < (F::kTileBytes + 511) / 512; ++i) {
-      const int unit = i * 32 + lane;
-      if (unit < F::kTileBytes / 16)
-        *reinterpret_cast<uint4*>(tile + unit * 16) =
-            *reinterpret_cast<const uint4*>(stage + (is_v ? stage_unit<D>(unit) : unit) * 16);
+      if (i * TPI + TPI <= t.r0 || i * TPI >= t.r1) continue;
+      const Quant16 g = quantise16(x[i]);
+      const int r = i * TPI + at;
+      if (r >= t.r0 && r < t.r1) store_token<D>(tile, is_v, r, j, hq, g);
     }
     return;
   }
-#pragma unroll 1
-  for (int i = t.r0 / TPI; i * TPI < t.r1; ++i) {  // a part of the tile: the other tokens' bits stay as they are
-    const int r = i * TPI + lane / LPR;
-    uint4 y = x[0];
+  // the whole tile: staged, so that it leaves in 16-byte stores
+  uint8_t* stage = stage_s[warp];
 #pragma unroll
-    for (int u = 1; u < NI; ++u) y = u == i ? x[u] : y;
-    const Quant8 g = quantise8(y);
-    if (r < t.r0 || r >= t.r1) continue;
-    if (is_v) {
-      *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q, j)) = uint16_t(g.word);
-      *reinterpret_cast<uint16_t*>(tile + F::v_half(r, 2 * q + 1, j)) = uint16_t(g.word >> 16);
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * TPI + at;
+    const Quant16 g = quantise16(x[i]);
+    if (is_v) {  // a word holds two tokens: the even one's lane puts together the first chunk's, the odd one's the second's
+      const bool odd = (r & 1) != 0;
+      const uint32_t own = odd ? g.word[1] : g.word[0];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? g.word[0] : g.word[1], LPR);
+      const uint32_t a0 = odd ? got : own, a1 = odd ? own : got;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int to = F::v_half(r & ~1, 2 * hq + 4 * (r & 1) + u, j);
+        *reinterpret_cast<uint32_t*>(stage + stage_unit<D>(to >> 4) * 16 + (to & 15)) = __byte_perm(a0, a1, u ? 0x7632 : 0x5410);
+      }
     } else {
-      *reinterpret_cast<uint32_t*>(tile + F::k_word(r, q, j)) = g.word;
+      *reinterpret_cast<uint32_t*>(stage + F::k_word(r, hq, j)) = g.word[0];
+      *reinterpret_cast<uint32_t*>(stage + F::k_word(r, hq + 2, j)) = g.word[1];
     }
-    if (q == 0) {
-      *reinterpret_cast<uint16_t*>(tile + (is_v ? F::v_step(r, j) : F::k_step(r, j))) = g.s;
-      *reinterpret_cast<uint16_t*>(tile + F::min_at(r, j)) = g.m;
+    if (hq == 0) {
+      *reinterpret_cast<uint16_t*>(stage + (is_v ? F::v_step(r, j) : F::k_step(r, j))) = g.s;
+      *reinterpret_cast<uint16_t*>(stage + F::min_at(r, j)) = g.m;
     }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < (F::kTileBytes + 511) / 512; ++i) {
+    const int unit = i * 32 + lane;
+    if (unit < F::kTileBytes / 16)
+      *reinterpret_cast<uint4*>(tile + unit * 16) =
+          *reinterpret_cast<const uint4*>(stage + (is_v ? stage_unit<D>(unit) : unit) * 16);
   }
 }
 
@@ -333,6 +368,24 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Args a, unsigned per, 
   }
 }
 
+// (x & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+
+// Nibbles 2 c and 2 c + 1 of a word as floats. A nibble at bit p is left where
+// it is: under the exponent of 2^(23 - p) it counts ones, and 2^(23 - p) comes
+// off exactly. Bits 20 and up are moved down by 12 first.
+__device__ __forceinline__ float2 nibble_pair(uint32_t w, int c) {
+  const uint32_t x = 2 * c >= 5 ? w >> 12 : w, y = 2 * c + 1 >= 5 ? w >> 12 : w;
+  const int px = 8 * c - (2 * c >= 5 ? 12 : 0), py = 8 * c + 4 - (2 * c + 1 >= 5 ? 12 : 0);
+  const uint32_t ex = uint32_t(127 + 23 - px) << 23, ey = uint32_t(127 + 23 - py) << 23;
+  return add_f32x2(make_float2(__uint_as_float(and_or(x, 15u << px, ex)), __uint_as_float(and_or(y, 15u << py, ey))),
+                   make_float2(-__uint_as_float(ex), -__uint_as_float(ey)));
+}
+
 // One warp per (sequence, KV head, candidate block). A lane sums the 8 tokens
 // g, g + 8, ... of its t, 8 channels per group; the lanes of a t are then added
 // pairwise, each keeping half of the channels.
@@ -373,12 +426,7 @@ __global__ void __launch_bounds__(128) kv4_means_kernel(Kv4Args a, unsigned per,
       const float sf = __uint_as_float((j & 1) ? s[i][j / 2] & 0xffff0000u : s[i][j / 2] << 16);
       low += __uint_as_float((j & 1) ? lo[i][j / 2] & 0xffff0000u : lo[i][j / 2] << 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // 2^23 + code has the code in its low bits
-        const float2 n = add_f32x2(make_float2(__uint_as_float(0x4b000000u | ((w[i][j] >> (8 * c)) & 15u)),
-                                               __uint_as_float(0x4b000000u | ((w[i][j] >> (8 * c + 4)) & 15u))),
-                                   dup2(-8388608.f));
-        acc[j][c] = fma_f32x2(n, dup2(sf), acc[j][c]);
-      }
+      for (int c = 0; c < 4; ++c) acc[j][c] = fma_f32x2(nibble_pair(w[i][j], c), dup2(sf), acc[j][c]);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[j][c] = add_f32x2(acc[j][c], dup2(low));
@@ -426,8 +474,8 @@ cudaError_t launch_kv4_write(const Shape& sh, const Cache& c, int n_tokens, cons
   const Kv4Args a = kv4_args(sh, c, n_tokens, cache_len, new_len, err);
   const unsigned per = tiles_of(n_tokens);
   unsigned n;
-  if (!kv4_grid(sh, per, 8, &n)) return cudaErrorInvalidConfiguration;
-  return launch_pdl(sh.d == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>, dim3(n, 2), dim3(256), 0, st, a, per, k, v);
+  if (!kv4_grid(sh, per, kWriteWarps, &n)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(sh.d == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>, dim3(n, 2), dim3(32 * kWriteWarps), 0, st, a, per, k, v);
 }
 
 cudaError_t launch_kv4_read(const Shape& sh, const Cache& c, int n_tokens, uint16_t* k, uint16_t* v,
