@@ -27,7 +27,6 @@
 // spin waits), its own running maximum. The warps' partials meet at the end.
 #include <cooperative_groups.h>
 
-#include "decode_select.cuh"
 #include "kv4.cuh"
 
 namespace sas {
@@ -37,10 +36,11 @@ using namespace kv4;
 
 namespace {
 
-constexpr int kWarps = dec::kThreads / 32;  // warps of a fused CTA
-constexpr int kSplitWarps = 4;              // warps of a split CTA
-constexpr int kSlots = 2;                   // record slots of a warp's ring
-constexpr int kMaxTasks = 256;      // blocks of one CTA's list (fused: the whole list of a row)
+constexpr int kWarps = 4;           // warps of a CTA
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCluster = 8;      // portable cluster size
+constexpr int kMaxPicks = 255;      // one-launch form: picks of a row
+constexpr int kWarpTasks = 128;     // tasks of a warp: 256 blocks in halves over the 4 warps of one CTA
 constexpr float kPShift = 8.f;      // P is kept times 2^8
 constexpr int kStepField = 17;      // exponent field that the largest step gets in fp16 when the base is set
 constexpr int kStepLimit = 23;      // a step with this field (2^8) moves the base: P·s stays under 2^16
@@ -59,7 +59,7 @@ struct Kv4DecodeArgs {
   uint16_t* o;             // one-launch form
   float* lse_o;            // may be null
   int* err;
-  int B, Hkv, G, Lmax, K, gate, gated, outside, need_lse, n_split;
+  int B, Hkv, G, Lmax, K, gate, gated, outside, n_split;
   float scale;
 };
 
@@ -171,12 +171,16 @@ struct Query {
   float2 over;           // factors of S before f where f alone would leave fp32's range (queries above 2^100)
   bool big;              // whether any head of the row has one
 
-  __device__ __forceinline__ void load(const uint16_t* q, int G, float scale) {
+  // This lane's channels of head g, as they are in memory.
+  static __device__ __forceinline__ void read(const uint16_t* q, int G, uint4 (&x)[NG]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint4 x[NG];
 #pragma unroll
     for (int j = 0; j < NG; ++j)
       x[j] = g < G ? *reinterpret_cast<const uint4*>(q + g * D + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+  }
+
+  __device__ __forceinline__ void make(const uint4 (&x)[NG], float scale) {
+    const int t = threadIdx.x & 3;
     uint32_t mx = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
     for (int j = 0; j < NG; ++j)
@@ -246,15 +250,15 @@ struct State {
   }
 };
 
-// S of a block's 64 tokens from its K record. With FULL, all of them count;
+// S of NT tiles of tokens from a K record. With FULL, all of them count;
 // otherwise those past ntok become -inf.
-template <int D, bool FULL>
-__device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& q, int ntok, float2 (&S)[kTiles][2]) {
+template <int D, int NT, bool FULL>
+__device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& q, int ntok, float2 (&S)[NT][2]) {
   using F = Fmt<D>;
   constexpr int NG = F::NG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
+  for (int i = 0; i < NT; ++i) {
     if (!FULL && 16 * i >= ntok) {
       S[i][0] = S[i][1] = make_float2(-INFINITY, -INFINITY);
       continue;
@@ -291,13 +295,13 @@ __device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& 
 
 // The online softmax: S becomes p · 2^8 with p = 2^(S f + lam - max), and the
 // state is rescaled. (f > 0, so the largest logit is that of the largest S.)
-template <int D>
-__device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[kTiles][2]) {
+template <int D, int NT>
+__device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[NT][2]) {
   float top[2], sub[2], al[2];
   top[0] = fmaxf(S[0][0].x, S[0][1].x);
   top[1] = fmaxf(S[0][0].y, S[0][1].y);
 #pragma unroll
-  for (int i = 1; i < kTiles; ++i) {
+  for (int i = 1; i < NT; ++i) {
     top[0] = fmaxf(top[0], fmaxf(S[i][0].x, S[i][1].x));
     top[1] = fmaxf(top[1], fmaxf(S[i][0].y, S[i][1].y));
   }
@@ -317,7 +321,7 @@ __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, f
   const float2 add = make_float2(sub[0], sub[1]);
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float2 z = fma_f32x2(S[i][u], q.f, add);
@@ -343,13 +347,13 @@ __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, f
 }
 
 // O += P V from the block's V record.
-template <int D, bool FULL>
-__device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, int ntok, const float2 (&p)[kTiles][2]) {
+template <int D, int NT, bool FULL>
+__device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, int ntok, const float2 (&p)[NT][2]) {
   using F = Fmt<D>;
   constexpr int NG = F::NG;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
+  for (int i = 0; i < NT; ++i) {
     if (!FULL && 16 * i >= ntok) break;
     const uint8_t* tile = rec + i * F::kTileBytes;
     uint32_t stp[NG][2];  // steps of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
@@ -408,185 +412,325 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
   }
 }
 
-// A warp's ring of records. Item 2 i is block i's K, item 2 i + 1 its V; an
-// item's slot is refilled as soon as it has been used.
-template <int D>
-__device__ __forceinline__ void ring_issue(uint8_t* ring, const Cache& c, int item, int slot, int rec, int ntok) {
-  using F = Fmt<D>;
-  const int lane = threadIdx.x & 31;
-  const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(rec) * F::kRecord + lane * 16;
-  const uint32_t dst = smem_u32(ring) + slot * F::kRecord + lane * 16;
-  if (ntok == kBlock) {
-#pragma unroll
-    for (int o = 0; o < F::kRecord; o += 512) cp_async16(dst + o, src + o);
-  } else {  // the tiles that hold tokens
-    const int bytes = (ntok + kTile - 1) / kTile * F::kTileBytes;
-#pragma unroll 1
-    for (int o = 0; o + lane * 16 < bytes; o += 512) cp_async16(dst + o, src + o);
-  }
-}
+// A warp's ring: tasks of NT tiles (a block, or half of one), NT tiles of K in
+// one slot and of V in the next. Item 2 i is task i's K, item 2 i + 1 its V; a
+// slot is refilled as soon as it has been used. A task is named by its place
+// among the cache's NT-tile units (-1: a block that is left out).
+template <int D, int NT>
+struct Ring {
+  static constexpr int kParts = kTiles / NT;              // tasks of a block
+  static constexpr int kSlots = 2 * kParts;               // a block's K and V in all
+  static constexpr int kSlotBytes = NT * Fmt<D>::kTileBytes;
+  static constexpr int kBytes = kSlots * kSlotBytes;
 
-// Runs a warp over blocks first, first + W, ... < n of its CTA's list
-// (records rec_s, -1 for a block that is left out; gates lam_s). The item
-// numbered `issued` is the first that is not yet under way.
-template <int D, int W>
-__device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
-                                           const int* rec_s, const float* lam_s, int first, int n, int cur_at,
-                                           int cur_ntok, int issued) {
-  const int mine = n > first ? (n - 1 - first) / W + 1 : 0;
-  auto issue = [&](int item, int slot) {
-    if (item < 2 * mine) {
-      const int at = first + (item >> 1) * W;
-      const int rec = rec_s[at];
-      if (rec >= 0) ring_issue<D>(ring, a.c, item, slot, rec, at == cur_at ? cur_ntok : kBlock);
+  static __device__ __forceinline__ void issue(uint8_t* ring, const Cache& c, int item, int unit, int ntok) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(unit) * kSlotBytes + lane * 16;
+    const uint32_t dst = smem_u32(ring) + (item & (kSlots - 1)) * kSlotBytes + lane * 16;
+    if (ntok == NT * kTile) {
+#pragma unroll
+      for (int o = 0; o < kSlotBytes; o += 512)
+        if (kSlotBytes % 512 == 0 || o + lane * 16 < kSlotBytes) cp_async16(dst + o, src + o);
+    } else {  // the tiles that hold tokens
+      const int bytes = (ntok + kTile - 1) / kTile * Fmt<D>::kTileBytes;
+#pragma unroll 1
+      for (int o = 0; o + lane * 16 < bytes; o += 512) cp_async16(dst + o, src + o);
+    }
+  }
+  // Items from `item` on, up to a full ring, each its own copy group.
+  static __device__ __forceinline__ void fill(uint8_t* ring, const Cache& c, const int* unit_s, int n, int ntok0, int item) {
+    for (; item < kSlots; ++item) step(ring, c, unit_s, n, ntok0, item);
+  }
+  static __device__ __forceinline__ void step(uint8_t* ring, const Cache& c, const int* unit_s, int n, int ntok0, int item) {
+    if (item < 2 * n) {
+      const int unit = unit_s[item >> 1];
+      if (unit >= 0) issue(ring, c, item, unit, item < 2 ? ntok0 : NT * kTile);
     }
     cp_async_commit();
-  };
-  for (int k = issued; k < kSlots; ++k) issue(k, k);
-  int slot = 0;
-  auto next = [&] {
-    slot = slot + 1 == kSlots ? 0 : slot + 1;
-  };
-  for (int i = 0; i < mine; ++i) {
-    const int at = first + i * W;
-    const int ntok = rec_s[at] < 0 ? 0 : at == cur_at ? cur_ntok : kBlock;
-    const float lam = lam_s[at];
-    float2 S[kTiles][2];
-    cp_async_wait<kSlots - 1>();
+  }
+};
+
+// A warp over its n tasks: units unit_s, gates lam_s (log2). The first task has
+// ntok0 tokens, the others all. The ring has been filled.
+template <int D, int NT>
+__device__ __forceinline__ void run_tasks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
+                                          const int* unit_s, const float* lam_s, int n, int ntok0) {
+  using R = Ring<D, NT>;
+  for (int i = 0; i < n; ++i) {
+    const int ntok = unit_s[i] < 0 ? 0 : i == 0 ? ntok0 : NT * kTile;
+    const float lam = a.gated ? lam_s[i] : 0.f;
+    float2 S[NT][2];
+    cp_async_wait<R::kSlots - 1>();
     __syncwarp();
-    const uint8_t* rec = ring + slot * Fmt<D>::kRecord;
-    if (ntok == kBlock)
-      score_block<D, true>(rec, q, ntok, S);
+    const uint8_t* rec = ring + (2 * i & (R::kSlots - 1)) * R::kSlotBytes;
+    if (ntok == NT * kTile)
+      score_block<D, NT, true>(rec, q, ntok, S);
     else
-      score_block<D, false>(rec, q, ntok, S);
+      score_block<D, NT, false>(rec, q, ntok, S);
     __syncwarp();
-    issue(2 * i + kSlots, slot);
-    next();
-    softmax_block<D>(st, q, a.outside ? 0.f : lam, S);
+    R::step(ring, a.c, unit_s, n, ntok0, 2 * i + R::kSlots);
+    softmax_block<D, NT>(st, q, a.outside ? 0.f : lam, S);
     if (a.outside) {
       const float gw = exp2f(lam);
 #pragma unroll
-      for (int k = 0; k < kTiles; ++k)
+      for (int k = 0; k < NT; ++k)
 #pragma unroll
         for (int u = 0; u < 2; ++u) S[k][u] = make_float2(S[k][u].x * gw, S[k][u].y * gw);
     }
-    cp_async_wait<kSlots - 1>();
+    cp_async_wait<R::kSlots - 1>();
     __syncwarp();
-    rec = ring + slot * Fmt<D>::kRecord;
-    if (ntok == kBlock)
-      value_block<D, true>(rec, st, ntok, S);
+    rec += R::kSlotBytes;  // the number of slots is even
+    if (ntok == NT * kTile)
+      value_block<D, NT, true>(rec, st, ntok, S);
     else
-      value_block<D, false>(rec, st, ntok, S);
+      value_block<D, NT, false>(rec, st, ntok, S);
     __syncwarp();
-    issue(2 * i + 1 + kSlots, slot);
-    next();
+    R::step(ring, a.c, unit_s, n, ntok0, 2 * i + 1 + R::kSlots);
   }
   cp_async_wait<0>();
 }
 
-// A warp's partial in shared memory: per head D normalised outputs, then the
-// maximum and the sum.
+// The merge of a row's (or a split's) partials over CS CTAs. A warp's partial
+// is G x D normalised outputs in units of 4 channels, with the maximum and the
+// sum of every head. Unit u is merged by CTA u % CS: the warps store their
+// units straight into its shared memory, so that one cluster barrier is enough
+// and no CTA reads another's memory.
 template <int D>
-struct Partial {
-  float o[8][D];
-  float m[8], l[8];
+struct Merge {
+  int CS, rank, U;    // U units per CTA
+  unsigned magic;     // u / CS = u * magic >> 16 for u < 256
+  float4* o;          // [warp of the cluster][U]
+  float2* ml;         // [warp of the cluster][8 heads]
+
+  static __host__ __device__ int units(int G, int CS) { return (G * D / 4 + CS - 1) / CS; }
+  static __host__ __device__ int bytes(int G, int CS) { return CS * kWarps * (units(G, CS) * 16 + 64); }
+
+  __device__ __forceinline__ Merge(uint8_t* smem, int G, int CS, int rank)
+      : CS(CS), rank(rank), U(units(G, CS)), magic(65536u / unsigned(CS) + 1u), o(reinterpret_cast<float4*>(smem)),
+        ml(reinterpret_cast<float2*>(smem + CS * kWarps * U * 16)) {}
+
+  template <bool CLUSTER>
+  __device__ __forceinline__ void push(const State<D>& st, int G) const {
+    constexpr int NG = D / kGroup;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, from = rank * kWarps + int(threadIdx.x >> 5);
+    const float f = exp2f(float(int((st.lo & 0xffffu) >> 7) - 112));
+    float l[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] = st.l[h];
+#pragma unroll
+      for (int x = 4; x <= 16; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+      const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+      const int head = 2 * t + h;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        float am = h ? st.accm[j].y : st.accm[j].x;
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) am += __shfl_xor_sync(0xffffffffu, am, x);
+        am *= inv;
+        float4 v;
+        v.x = fmaf(st.acc[j][0][h] * (inv * 16777216.f), f, am);
+        v.y = fmaf(st.acc[j][0][2 + h] * (inv * 1048576.f), f, am);
+        v.z = fmaf(st.acc[j][1][h] * (inv * 16777216.f), f, am);
+        v.w = fmaf(st.acc[j][1][2 + h] * (inv * 1048576.f), f, am);
+        if (head < G) {
+          const int u = head * (D / 4) + 8 * j + g, slot = int(unsigned(u) * magic >> 16), owner = u - slot * CS;
+          float4* dst = o + from * U + slot;
+          if (CLUSTER) dst = cg::this_cluster().map_shared_rank(dst, owner);
+          *dst = v;
+        }
+      }
+    }
+    if (g < CS) {
+      float4* dst = reinterpret_cast<float4*>(ml + from * 8 + 2 * t);
+      if (CLUSTER) dst = cg::this_cluster().map_shared_rank(dst, g);
+      *dst = make_float4(st.m[0], l[0], st.m[1], l[1]);
+    }
+  }
+
+  // Eight lanes to a unit; out(head, channel, outputs, lse) stores it. A row
+  // whose sum is NaN in any partial is NaN.
+  template <typename Out>
+  __device__ __forceinline__ void run(int G, Out out) const {
+    const int sub = threadIdx.x & 7, n = CS * kWarps;
+    for (int base = 0; base < U; base += kThreads / 8) {
+      const int s = base + int(threadIdx.x >> 3), u = s * CS + rank;
+      const bool live = s < U && u < G * D / 4;
+      const int head = live ? u / (D / 4) : 0;
+      float M = -INFINITY;
+      for (int w = sub; w < n; w += 8) M = fmaxf(M, ml[w * 8 + head].x);
+#pragma unroll
+      for (int x = 1; x <= 4; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      const float ref = M == -INFINITY ? 0.f : M;
+      float den = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = sub; w < n; w += 8) {
+        const float2 p = ml[w * 8 + head];
+        if (p.y == 0.f) continue;  // a warp without tokens
+        const float k = p.y * exp2f(p.x - ref);
+        const float4 y = o[w * U + (live ? s : 0)];
+        den += k;
+        v.x = fmaf(k, y.x, v.x);
+        v.y = fmaf(k, y.y, v.y);
+        v.z = fmaf(k, y.z, v.z);
+        v.w = fmaf(k, y.w, v.w);
+      }
+#pragma unroll
+      for (int x = 1; x <= 4; x <<= 1) {
+        den += __shfl_xor_sync(0xffffffffu, den, x);
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, x);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, x);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, x);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, x);
+      }
+      if (!live || sub != 0) continue;
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      out(head, 4 * (u % (D / 4)), make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv),
+          den == 0.f ? -INFINITY : (M + log2f(den) - kPShift) * kLn2);
+    }
+  }
 };
 
-template <int D>
-__device__ __forceinline__ void store_partial(const State<D>& st, Partial<D>* out) {
-  constexpr int NG = D / kGroup;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const float f = exp2f(float(int((st.lo & 0xffffu) >> 7) - 112));
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float l = st.l[h];
-#pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      float am = h ? st.accm[j].y : st.accm[j].x;
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) am += __shfl_xor_sync(0xffffffffu, am, o);
-      am *= inv;
-      float4 v;
-      v.x = fmaf(st.acc[j][0][h] * (inv * 16777216.f), f, am);
-      v.y = fmaf(st.acc[j][0][2 + h] * (inv * 1048576.f), f, am);
-      v.z = fmaf(st.acc[j][1][h] * (inv * 16777216.f), f, am);
-      v.w = fmaf(st.acc[j][1][2 + h] * (inv * 1048576.f), f, am);
-      *reinterpret_cast<float4*>(&out->o[2 * t + h][32 * j + 4 * g]) = v;
-    }
-    if (g == 0) {
-      out->m[2 * t + h] = st.m[h];
-      out->l[2 * t + h] = l;
-    }
-  }
+// The first barrier of a cluster (its CTAs have started: their memory may be
+// written), and the second (what was written is there).
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// Output `col`, `col` + 1 of head g, merged from n partials. A row whose sum is
-// NaN in any of them is NaN. Returns the sum relative to M (times 2^8).
-template <int D, typename At>
-__device__ __forceinline__ float merge_partials(At at, int n, int g, int col, float2& o, float& M) {
-  M = -INFINITY;
-  for (int r = 0; r < n; ++r) M = fmaxf(M, at(r)->m[g]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float den = 0.f;
-  o = make_float2(0.f, 0.f);
-  for (int r = 0; r < n; ++r) {
-    const Partial<D>* p = at(r);
-    const float l = p->l[g];
-    const float w = l == 0.f ? 0.f : l * exp2f(p->m[g] - ref);
-    const float2 v = *reinterpret_cast<const float2*>(&p->o[g][col]);
-    den += w;
-    o.x = l == 0.f ? o.x : fmaf(w, v.x, o.x);
-    o.y = l == 0.f ? o.y : fmaf(w, v.y, o.y);
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  o.x *= inv;
-  o.y *= inv;
-  return den;
-}
-__device__ __forceinline__ float lse_of(float M, float den) {
-  return den == 0.f ? -INFINITY : (M + log2f(den) - kPShift) * kLn2;
+// The score that has an orderable key.
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// Dynamic shared memory of a CTA of W warps: the rings, and the partials in their place.
-template <int D, int W>
-constexpr int smem_bytes() {
-  constexpr int ring = W * kSlots * Fmt<D>::kRecord, part = W * int(sizeof(Partial<D>));
-  return ring > part ? ring : part;
-}
+// One warp's Top-K of a score row, without a block-wide barrier: lane i holds
+// the keys of blocks i, 32 + i, ... in registers. A bisection between the
+// smallest and the largest key finds a threshold with n keys at or above it, in
+// a dozen counts of the row: at first it halves the range of values, which
+// spread evenly over their own range, and after 16 steps that of keys, which
+// ends for sure. Where a tie is cut, it ends on the tied key.
+template <int CAP>
+struct Row {
+  uint32_t key[CAP];  // orderable key + 1, 0 past the history
+
+  __device__ __forceinline__ void read(const float* s, int NB) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) key[i] = 32 * i + lane < NB ? __float_as_uint(__ldg(s + 32 * i + lane)) : 0u;
+  }
+  __device__ __forceinline__ void make(int c) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) key[i] = 32 * i + lane < c ? score_key(__uint_as_float(key[i])) + 1u : 0u;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) k = max(k, key[i]);
+    return __reduce_max_sync(0xffffffffu, k);
+  }
+  // log Σ exp of the row's scores, as the select kernels take it
+  __device__ __forceinline__ float lse(int c) const {
+    const uint32_t k = top();
+    const float mx = k <= 1u ? -INFINITY : key_score(k - 1u);
+    if (mx == -INFINITY) return -INFINITY;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i)
+      if (32 * i < c && key[i] != 0u) sum += expf(key_score(key[i] - 1u) - mx);
+    return mx + logf(warp_sum(sum));
+  }
+  // The n highest of the c blocks (ties to the lower block), ascending, to sel.
+  __device__ __forceinline__ void select(int c, int n, int* sel) const {
+    const int lane = threadIdx.x & 31;
+    uint32_t thr = 1u, tied = 0u;  // taken: keys >= thr, and the first `need` that equal tied
+    int need = 0;
+    if (n < c) {
+      uint32_t lo = 0xffffffffu, hi = top() + 1u;  // count(lo) > n > count(hi)
+#pragma unroll
+      for (int i = 0; i < CAP; ++i) lo = min(lo, key[i] - 1u);
+      lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
+      int above = 0;  // count(hi)
+      for (int round = 0;; ++round) {
+        if (hi - lo <= 1u) {
+          thr = hi;
+          tied = lo;
+          need = n - above;
+          break;
+        }
+        uint32_t mid = lo + (hi - lo) / 2u;
+        if (round < 16) {
+          const uint32_t v = score_key(0.5f * key_score(lo - 1u) + 0.5f * key_score(hi - 1u)) + 1u;
+          if (v > lo && v < hi) mid = v;
+        }
+        int cnt = 0;
+#pragma unroll
+        for (int i = 0; i < CAP; ++i)
+          if (CAP <= 16 || 32 * i < c) cnt += key[i] >= mid ? 1 : 0;
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (cnt == n) {
+          thr = mid;
+          break;
+        }
+        if (cnt > n) {
+          lo = mid;
+        } else {
+          hi = mid;
+          above = cnt;
+        }
+      }
+    }
+    const unsigned below = (1u << lane) - 1u;
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < CAP; ++i) {
+      if (32 * i >= c) break;
+      bool take = key[i] >= thr;
+      if (need > 0) {
+        const unsigned eq = __ballot_sync(0xffffffffu, key[i] == tied);
+        take = take || (key[i] == tied && __popc(eq & below) < need);
+        need -= min(need, __popc(eq));
+      }
+      const unsigned b = __ballot_sync(0xffffffffu, take);
+      if (take) sel[base + __popc(b & below)] = 32 * i + lane;
+      base += __popc(b);
+    }
+  }
+};
 
 }  // namespace
 
-// One CTA per (sequence, KV head, split), or a cluster of CS (CLUSTER) whose
-// CTAs take every CS-th block of the split's run.
-template <int D, bool CLUSTER>
-__global__ void __launch_bounds__(32 * kSplitWarps, 16 / kSplitWarps) kv4_decode_split_kernel(Kv4DecodeArgs a) {
-  using F = Fmt<D>;
-  constexpr int W = kSplitWarps;
+// One CTA per (sequence, KV head, split), or a cluster of CS. The tasks of the
+// split's run go round the cluster's warps.
+template <int D, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4DecodeArgs a) {
+  using R = Ring<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int rec_s[kMaxDecodeBlocksPerSplit];
-  __shared__ float lam_s[kMaxDecodeBlocksPerSplit];
+  __shared__ int unit_s[kWarps][kMaxDecodeBlocksPerSplit * R::kParts / kWarps];
+  __shared__ float lam_s[kWarps][kMaxDecodeBlocksPerSplit * R::kParts / kWarps];
   const int CS = CLUSTER ? int(cg::this_cluster().num_blocks()) : 1;
   const int rank = CLUSTER ? int(cg::this_cluster().block_rank()) : 0;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps, worker = warp * CS + rank;
   const int item = blockIdx.x / CS, split = item % a.n_split, bh = item / a.n_split, b = bh / a.Hkv, h = bh % a.Hkv;
   const int NB = a.Lmax / kBlock;
-  uint8_t* ring = smem + warp * kSlots * F::kRecord;
+  uint8_t* ring = smem + warp * R::kBytes;
+  if (CLUSTER) cluster_begin();
   griddep_launch_dependents();  // the merge kernel may begin its launch; it waits for this grid's writes
   griddep_wait();               // idx and lse_s come from the select kernel that precedes this one
   int L = a.cache_len[b];
+  uint4 raw[D / kGroup];
+  Query<D>::read(a.q + size_t(bh) * a.G * D, a.G, raw);
   if (L < 1 || L > a.Lmax) {
     if (tid == 0) raise_error(a.err, SAS_ERR_DEVICE_INDEX);
     L = max(1, min(L, a.Lmax));
   }
   const int c = (L - 1) / kBlock, nl = 1 + min(a.K, c);
   const int per = (nl + a.n_split - 1) / a.n_split;
-  const int lo = min(split * per, nl), n = min(lo + per, nl) - lo;
-  const int nt = rank < n ? (n - 1 - rank) / CS + 1 : 0;
-  if (tid < nt) {
-    const int pos = lo + tid * CS + rank;
+  const int lo = min(split * per, nl), tasks = (min(lo + per, nl) - lo) * R::kParts;
+  const int n = worker < tasks ? (tasks - 1 - worker) / W + 1 : 0;
+  for (int k = lane; k < n; k += 32) {
+    const int task = k * W + worker, pos = lo + task / R::kParts;
     int m = c;
     float lam = 0.f;
     if (pos > 0) {
@@ -598,178 +742,120 @@ __global__ void __launch_bounds__(32 * kSplitWarps, 16 / kSplitWarps) kv4_decode
         lam = gate_lam2(a.gate, a.s[size_t(bh) * NB + m], a.lse_s_in != nullptr ? a.lse_s_in[bh] : 0.f);
     }
     const int rec = m < 0 ? -1 : record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-    rec_s[tid] = rec;
-    lam_s[tid] = rec < 0 ? 0.f : lam;
+    unit_s[warp][k] = rec < 0 ? -1 : rec * R::kParts + task % R::kParts;
+    lam_s[warp][k] = rec < 0 ? 0.f : lam;
   }
+  __syncwarp();
+  // tokens of the first task: the current block's, if it is one of its parts
+  const int ntok0 = lo == 0 && worker < R::kParts ? max(0, min(NT * kTile, L - c * kBlock - worker * NT * kTile)) : NT * kTile;
+  R::fill(ring, a.c, unit_s[warp], n, ntok0, 0);
   Query<D> q;
-  q.load(a.q + size_t(bh) * a.G * D, a.G, a.scale);
+  q.make(raw, a.scale);
   State<D> st;
   st.clear();
-  __syncthreads();
-  run_blocks<D, W>(a, st, q, ring, rec_s, lam_s, warp, nt, lo == 0 && rank == 0 ? 0 : -1, L - c * kBlock, 0);
-  __syncthreads();  // the rings are done with
-  Partial<D>* part = reinterpret_cast<Partial<D>*>(smem);
-  store_partial<D>(st, part + warp);
-  if (CLUSTER)
-    cg::this_cluster().sync();  // every partial of the cluster is in place
-  else
+  run_tasks<D, NT>(a, st, q, ring, unit_s[warp], lam_s[warp], n, ntok0);
+  const Merge<D> mg(CLUSTER ? smem + kWarps * R::kBytes : smem, a.G, CS, rank);
+  if (CLUSTER) {
+    cluster_begun();
+    mg.template push<true>(st, a.G);
+    cluster_sync();
+  } else {
+    __syncthreads();  // the rings are done with, and the partials take their place
+    mg.template push<false>(st, a.G);
     __syncthreads();
-  for (int e = rank * 32 * W + tid; e < a.G * D / 2; e += CS * 32 * W) {
-    const int g = 2 * e / D, col = 2 * e % D;
-    float2 o;
-    float M;
-    const float den = merge_partials<D>(
-        [&](int r) { return CLUSTER ? cg::this_cluster().map_shared_rank(part, r / W) + r % W : part + r; }, CS * W, g,
-        col, o, M);
-    const size_t row = (size_t(bh) * a.G + g) * a.n_split + split;
-    *reinterpret_cast<float2*>(a.o_part + row * D + col) = o;
-    if (col == 0) a.lse_part[row] = lse_of(M, den);
   }
-  if (CLUSTER) cg::this_cluster().sync();  // no CTA leaves while another may still read its partials
+  mg.run(a.G, [&](int head, int col, float4 o, float lse) {
+    const size_t row = (size_t(bh) * a.G + head) * a.n_split + split;
+    *reinterpret_cast<float4*>(a.o_part + row * D + col) = o;
+    if (col == 0) a.lse_part[row] = lse;
+  });
 }
 
-// One cluster per (sequence, KV head): each CTA selects the row's blocks
-// itself and takes every CS-th one.
-template <int D>
-__global__ void __launch_bounds__(dec::kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
-  using F = Fmt<D>;
+// One cluster per (sequence, KV head). Every warp selects the row's blocks
+// itself, in registers, and takes every W-th task of the list [current block,
+// picks...]: there is no block-wide barrier before the merge, and the
+// redundant selection is cheaper than a hand-over.
+template <int D, int NT, int CAP>
+__global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
+  using R = Ring<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sel_s[dec::kFusedMaxK];
-  __shared__ int rec_s[kMaxTasks];
-  __shared__ float lam_s[kMaxTasks];
-  __shared__ int xch_s[4], wtot_s[kWarps], napp_s;
-  __shared__ float redf_s[kWarps];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int CS = int(cluster.num_blocks()), rank = int(cluster.block_rank());
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int sel_s[kWarps][kMaxPicks + 1];
+  __shared__ int unit_s[kWarps][kWarpTasks];
+  __shared__ float lam_s[kWarps][kWarpTasks];
+  const int CS = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps, worker = warp * CS + rank;
   const int bh = int(blockIdx.x) / CS, b = bh / a.Hkv, h = bh % a.Hkv;
   const int NB = a.Lmax / kBlock;
-  uint8_t* ring = smem + warp * kSlots * F::kRecord;
-  // the keys lie in the rings of warps 1 to 3, behind warp 0's, which starts on the current block at once
-  static_assert((kWarps - 1) * kSlots * F::kRecord >= dec::kFusedMaxNB * 4 + 768 * 4, "keys, histogram, picks, candidates");
-  uint32_t* key_s = reinterpret_cast<uint32_t*>(smem + kSlots * F::kRecord);
-  int* hist_s = reinterpret_cast<int*>(key_s + dec::kFusedMaxNB);
-  int* app_s = hist_s + 256;
-  uint32_t* cand_k = reinterpret_cast<uint32_t*>(app_s + 256);
-  int* cand_m = app_s + 384;
-  griddep_launch_dependents();
-  if (tid == 0) napp_s = 0;
-  griddep_wait();
-  // the row's scores are read while the cache length is still in flight
+  uint8_t* ring = smem + warp * R::kBytes;
   const float* srow = a.s + size_t(bh) * NB;
-  for (int m = tid; m < NB - 1; m += dec::kThreads) key_s[m] = __float_as_uint(__ldg(srow + m));
+  cluster_begin();
+  griddep_launch_dependents();
+  griddep_wait();
   int L = a.cache_len[b];
+  Row<CAP> row;
+  row.read(srow, NB);
+  uint4 raw[D / kGroup];
+  Query<D>::read(a.q + size_t(bh) * a.G * D, a.G, raw);
+  if (a.c.table != nullptr && tid * 32 < NB)  // the row's pages, for the lookup of the picks
+    asm volatile("prefetch.global.L1 [%0];\n" ::"l"(a.c.table + size_t(b) * NB + tid * 32));
   if (L < 1 || L > a.Lmax) {
     if (tid == 0) raise_error(a.err, SAS_ERR_DEVICE_INDEX);
     L = max(1, min(L, a.Lmax));
   }
-  const int c = (L - 1) / kBlock, n = min(a.K, c), nl = 1 + n;
-  const int nt = rank < nl ? (nl - 1 - rank) / CS + 1 : 0;  // list positions rank, rank + CS, ...
-  int issued = 0;
-  if (rank == 0 && warp == 0) {  // the current block needs no selection
+  const int c = (L - 1) / kBlock, n_pick = min(a.K, c), tasks = (1 + n_pick) * R::kParts;
+  const int n = worker < tasks ? (tasks - 1 - worker) / W + 1 : 0;
+  const bool has_cur = worker < R::kParts;
+  const int ntok0 = has_cur ? max(0, min(NT * kTile, L - c * kBlock - worker * NT * kTile)) : NT * kTile;
+  if (has_cur) {  // the current block needs no selection
     const int rec = record_of(a.c, b, h, c, a.Hkv, NB, a.err);
-    if (lane == 0) {
-      rec_s[0] = rec;
-      lam_s[0] = 0.f;
-    }
+    const int unit = rec < 0 ? -1 : rec * R::kParts + worker;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (rec >= 0) ring_issue<D>(ring, a.c, k, k, rec, L - c * kBlock);
+    for (int item = 0; item < 2; ++item) {
+      if (unit >= 0) R::issue(ring, a.c, item, unit, ntok0);
       cp_async_commit();
     }
-    issued = 2;
   }
-  float mx = -INFINITY;
-  for (int m = tid; m < c; m += dec::kThreads) {  // each thread converts the scores it read
-    const float v = __uint_as_float(key_s[m]);
-    key_s[m] = score_key(v) + 1u;  // >= 1, so the threshold 1 takes every block
-    mx = fmaxf(mx, v);
+  row.make(c);
+  row.select(c, n_pick, sel_s[warp]);
+  __syncwarp();
+  for (int k = lane; k < n; k += 32) {
+    const int task = k * W + worker, pos = task / R::kParts;
+    const int m = pos > 0 ? sel_s[warp][pos - 1] : c;
+    const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
+    unit_s[warp][k] = rec < 0 ? -1 : rec * R::kParts + task % R::kParts;
+    if (a.gated) lam_s[warp][k] = rec < 0 || pos == 0 ? 0.f : __ldg(srow + m);
   }
+  __syncwarp();
+  R::fill(ring, a.c, unit_s[warp], n, ntok0, has_cur ? 2 : 0);
+  // while the records are on their way: the queries, the gates and the row's outputs
   Query<D> q;
-  q.load(a.q + size_t(bh) * a.G * D, a.G, a.scale);
+  q.make(raw, a.scale);
+  const bool first = rank == 0 && warp == 0;
+  const bool soft = a.gate == SAS_GATE_LOG_SOFTMAX || a.gate == SAS_GATE_SOFTMAX_OUTSIDE;
   float lse = 0.f;
-  if (a.need_lse) {  // LSE of the history scores, as the select kernels take it
-    mx = warp_max(mx);
-    if (lane == 0) redf_s[warp] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(redf_s[0], redf_s[1]), fmaxf(redf_s[2], redf_s[3]));
-    __syncthreads();
-    float sum = 0.f;
-    if (mx != -INFINITY)
-      for (int m = tid; m < c; m += dec::kThreads) sum += expf(__ldg(srow + m) - mx);
-    sum = warp_sum(sum);
-    if (lane == 0) redf_s[warp] = sum;
-    __syncthreads();
-    const float tot = (redf_s[0] + redf_s[1]) + (redf_s[2] + redf_s[3]);
-    lse = (c == 0 || mx == -INFINITY) ? -INFINITY : mx + logf(tot);
+  if (soft || (first && a.lse_s_out != nullptr)) lse = row.lse(c);
+  if (a.gated) {
+    for (int k = lane; k < n; k += 32)
+      if (unit_s[warp][k] >= 0 && (k > 0 || !has_cur)) lam_s[warp][k] = gate_lam2(a.gate, lam_s[warp][k], lse);
+    __syncwarp();
   }
-  __syncthreads();  // every key is in place
-  int32_t* idx_row = (rank == 0 && a.idx_out != nullptr) ? a.idx_out + size_t(bh) * a.K : nullptr;
-  // list position pos holds block m: this CTA's task, if it is
-  auto place = [&](int pos, int m) {
-    if (idx_row != nullptr) idx_row[pos - 1] = m;
-    if (pos % CS == rank) {
-      const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-      rec_s[pos / CS] = rec;
-      lam_s[pos / CS] = a.gated && rec >= 0 ? gate_lam2(a.gate, __ldg(srow + m), lse) : 0.f;
-    }
-  };
-  if (n == c) {
-    for (int m = tid; m < c; m += dec::kThreads) place(m + 1, m);
-  } else {
-    uint32_t thr = 1u;
-    int need_eq = 0;
-    if (!cta_select(key_s, c, n, hist_s, xch_s, app_s, &napp_s, cand_k, cand_m, &xch_s[3], thr, need_eq)) {
-      __syncthreads();
-      for (int i = tid; i < n; i += dec::kThreads) {
-        const int v = app_s[i];
-        int r = 0;
-        for (int j = 0; j < n; ++j) r += app_s[j] < v ? 1 : 0;
-        place(r + 1, v);
-      }
-    } else {
-      // ties cut at the threshold, taken from the lowest block index: each thread
-      // owns a contiguous run of blocks, and two block-wide scans place the picks
-      const int per = (c + dec::kThreads - 1) / dec::kThreads;
-      const int lo = min(c, tid * per), hi = min(c, lo + per);
-      int eq = 0, tot = 0, take = 0;
-      for (int m = lo; m < hi; ++m) eq += key_s[m] == thr ? 1 : 0;
-      const int eq0 = cta_excl_sum(eq, wtot_s, tot);
-      for (int m = lo, e = eq0; m < hi; ++m) {
-        const bool is_eq = key_s[m] == thr;
-        take += (key_s[m] > thr || (is_eq && e < need_eq)) ? 1 : 0;
-        e += is_eq ? 1 : 0;
-      }
-      int pos = cta_excl_sum(take, wtot_s, tot);
-      for (int m = lo, e = eq0; m < hi; ++m) {
-        const bool is_eq = key_s[m] == thr;
-        if (key_s[m] > thr || (is_eq && e < need_eq)) place(++pos, m);
-        e += is_eq ? 1 : 0;
-      }
-    }
+  if (first) {
+    if (a.lse_s_out != nullptr && lane == 0) a.lse_s_out[bh] = lse;
+    if (a.idx_out != nullptr)
+      for (int i = lane; i < a.K; i += 32) a.idx_out[size_t(bh) * a.K + i] = i < n_pick ? sel_s[warp][i] : -1;
   }
-  if (idx_row != nullptr)
-    for (int i = n + tid; i < a.K; i += dec::kThreads) idx_row[i] = -1;
-  if (rank == 0 && a.lse_s_out != nullptr && tid == 0) a.lse_s_out[bh] = lse;
-  __syncthreads();  // the tasks are placed, and the keys' rings are free
   State<D> st;
   st.clear();
-  run_blocks<D, kWarps>(a, st, q, ring, rec_s, lam_s, warp, nt, rank == 0 ? 0 : -1, L - c * kBlock, issued);
-  __syncthreads();  // the rings are done with
-  Partial<D>* part = reinterpret_cast<Partial<D>*>(smem);
-  store_partial<D>(st, part + warp);
-  cluster.sync();  // every partial of the cluster is in place
-  for (int e = rank * dec::kThreads + tid; e < a.G * D / 2; e += CS * dec::kThreads) {
-    const int g = 2 * e / D, col = 2 * e % D;
-    float2 o;
-    float M;
-    const float den = merge_partials<D>(
-        [&](int r) { return cluster.map_shared_rank(part, r / kWarps) + r % kWarps; }, CS * kWarps, g, col, o, M);
-    const size_t row = size_t(bh) * a.G + g;
-    *reinterpret_cast<uint32_t*>(a.o + row * D + col) = pack_bf16x2(o.x, o.y);
-    if (col == 0 && a.lse_o != nullptr) a.lse_o[row] = lse_of(M, den);
-  }
-  cluster.sync();  // no CTA leaves while another may still read its partials
+  run_tasks<D, NT>(a, st, q, ring, unit_s[warp], lam_s[warp], n, ntok0);
+  const Merge<D> mg(smem + kWarps * R::kBytes, a.G, CS, rank);
+  cluster_begun();
+  mg.template push<true>(st, a.G);
+  cluster_sync();
+  mg.run(a.G, [&](int head, int col, float4 o, float ls) {
+    const size_t at = size_t(bh) * a.G + head;
+    *reinterpret_cast<uint2*>(a.o + at * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    if (col == 0 && a.lse_o != nullptr) a.lse_o[at] = ls;
+  });
 }
 
 static Kv4DecodeArgs kv4_decode_args(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl,
@@ -792,23 +878,26 @@ static Kv4DecodeArgs kv4_decode_args(const Shape& sh, const uint16_t* q, const C
   return a;
 }
 
-// Launches `kern` on `items` clusters of cs CTAs, as a dependent launch.
-static cudaError_t launch_clusters(void (*kern)(Kv4DecodeArgs), int items, int cs, int threads, int smem, cudaStream_t st,
-                                   const Kv4DecodeArgs& a) {
+// Launches `kern` on `items` clusters of cs CTAs, as a dependent launch. cs = 0:
+// plain CTAs.
+static cudaError_t launch_ctas(void (*kern)(Kv4DecodeArgs), int items, int cs, int smem, cudaStream_t st,
+                               const Kv4DecodeArgs& a) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(items) * cs);
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3(unsigned(items) * max(cs, 1));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = cs > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
@@ -818,22 +907,26 @@ static cudaError_t multiprocessors(int* sms) {
   return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
+#ifndef KV4_NT_SPLIT
+#define KV4_NT_SPLIT 4
+#define KV4_NT_FUSED 2
+#endif
+
 // Split form. The cluster size: the largest power of two that keeps every CTA
-// resident at once (16 warps per SM), at most 8 and at most half the blocks of
-// a split.
+// resident at once (16 warps per SM), at most 8 and at most one warp per block
+// of a split.
 template <int D>
 static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int W = kSplitWarps, smem = smem_bytes<D, W>();
-  static_assert(smem <= 48 * 1024, "no opt-in needed");
+  constexpr int NT = KV4_NT_SPLIT, ring = kWarps * Ring<D, NT>::kBytes;
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
   const int items = a.B * a.Hkv * a.n_split, per = (a.K + a.n_split) / a.n_split;
-  const int want = min(min(dec::kMaxCluster, (per + W - 1) / W), sms * (16 / W) / items);
+  const int want = min(min(kMaxCluster, (per + kWarps - 1) / kWarps), sms * 4 / items);
   int cs = 1;
   while (cs * 2 <= want) cs *= 2;
-  if (cs == 1) return launch_pdl(kv4_decode_split_kernel<D, false>, dim3(items), dim3(32 * W), smem, st, a);
-  return launch_clusters(kv4_decode_split_kernel<D, true>, items, cs, 32 * W, smem, st, a);
+  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, NT, false>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
+  return launch_ctas(kv4_decode_split_kernel<D, NT, true>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
 }
 
 cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl, const float* s,
@@ -845,22 +938,20 @@ cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c
   a.n_split = n_split;
   a.o_part = o_part;
   a.lse_part = lse_part;
-  const cudaError_t e = sh.d == 128 ? launch_split<128>(a, st) : launch_split<64>(a, st);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return sh.d == 128 ? launch_split<128>(a, st) : launch_split<64>(a, st);
 }
 
-// The cluster size: as many CTAs per row as keep the grid in one wave of
-// resident CTAs, at most 8 and at most one per block of the list.
-template <int D>
+// One launch. The cluster size: as many CTAs per row as keep the grid in one
+// wave of resident CTAs, at most 8 and at most one warp per task of the list.
+template <int D, int CAP>
 static cudaError_t launch_fused(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int smem = smem_bytes<D, kWarps>();
-  static_assert(smem <= 48 * 1024, "no opt-in needed");
+  constexpr int NT = KV4_NT_FUSED, ring = kWarps * Ring<D, NT>::kBytes;
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  const int rows = a.B * a.Hkv;
-  const int cs = max(1, min(min(dec::kMaxCluster, a.K + 1), sms * 3 / rows));
-  return launch_clusters(kv4_decode_fused_kernel<D>, rows, cs, dec::kThreads, smem, st, a);
+  const int rows = a.B * a.Hkv, tasks = (a.K + 1) * Ring<D, NT>::kParts;
+  const int cs = max(1, min(min(kMaxCluster, (tasks + kWarps - 1) / kWarps), sms * 3 / rows));
+  return launch_ctas(kv4_decode_fused_kernel<D, NT, CAP>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
 }
 
 cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl,
@@ -871,9 +962,9 @@ cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Ca
   a.lse_s_out = lse_s;
   a.o = o;
   a.lse_o = lse_o;
-  a.need_lse = (lse_s != nullptr || sh.gate == SAS_GATE_LOG_SOFTMAX || sh.gate == SAS_GATE_SOFTMAX_OUTSIDE) ? 1 : 0;
-  const cudaError_t e = sh.d == 128 ? launch_fused<128>(a, st) : launch_fused<64>(a, st);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const bool small = sh.NB <= 16 * 32;
+  return sh.d == 128 ? (small ? launch_fused<128, 16>(a, st) : launch_fused<128, 64>(a, st))
+                     : (small ? launch_fused<64, 16>(a, st) : launch_fused<64, 64>(a, st));
 }
 
 }  // namespace sas
