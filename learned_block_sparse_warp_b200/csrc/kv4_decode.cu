@@ -117,6 +117,15 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+      "mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // -126 <= e <= 127
 __device__ __forceinline__ float exp2_approx(float x) {  // 2^x, relative error about 2^-22, 0 below 2^-126
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -189,25 +198,26 @@ struct Query {
     mx = max(mx & 0xffffu, mx >> 16);
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // exponent of the largest; a row of zeros or subnormals uses the smallest normal's
-    const int e = min(max(int(mx >> 7), 1), 254) - 127;
+    // Exponent of the largest. The factor 2^(15 - e) stays a normal number: a
+    // row under 2^-112 is raised by 2^127 only, which is far enough.
+    const int e = max(min(int(mx >> 7), 254) - 127, -112);
+    const float2 up = make_float2(exp2_int(15 - e), exp2_int(11 - e));  // the odd channels go in divided by 16
     float part[NG];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-      float v[8];
-      float sm = 0.f;
+      float2 v[4], sm2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // 2^(15 - e) in two factors, neither of which leaves fp32's range
-        v[2 * i] = lo_bf16(w[i]) * ldexpf(1.f, -e) * 32768.f;
-        v[2 * i + 1] = hi_bf16(w[i]) * ldexpf(1.f, -e) * 32768.f;
-        sm += v[2 * i] + v[2 * i + 1];
+        v[i] = mul_f32x2(make_float2(lo_bf16(w[i]), hi_bf16(w[i])), up);
+        sm2 = add_f32x2(sm2, v[i]);
       }
-      b[j][0][0] = pack_f16x2(v[0], v[4]);
-      b[j][0][1] = pack_f16x2(v[1] * 0.0625f, v[5] * 0.0625f);
-      b[j][1][0] = pack_f16x2(v[2], v[6]);
-      b[j][1][1] = pack_f16x2(v[3] * 0.0625f, v[7] * 0.0625f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b[j][i][0] = pack_f16x2(v[i].x, v[i + 2].x);
+        b[j][i][1] = pack_f16x2(v[i].y, v[i + 2].y);
+      }
+      float sm = fmaf(sm2.y, 16.f, sm2.x);
       sm += __shfl_xor_sync(0xffffffffu, sm, 1);
       sm += __shfl_xor_sync(0xffffffffu, sm, 2);
       sm *= 5.9604644775390625e-8f;  // 2^-24, the codes' scale
@@ -219,8 +229,8 @@ struct Query {
     sum[1] = NG == 4 ? pack_bf16x2(part[NG - 2], part[NG - 1]) : 0u;
     const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
     const float c = scale * kLog2e * 512.f;  // 2^24 / 2^15
-    f = make_float2(c * ldexpf(1.f, min(e0, 100)), c * ldexpf(1.f, min(e1, 100)));
-    over = make_float2(ldexpf(1.f, max(e0 - 100, 0)), ldexpf(1.f, max(e1 - 100, 0)));
+    f = make_float2(c * exp2_int(min(e0, 100)), c * exp2_int(min(e1, 100)));
+    over = make_float2(exp2_int(max(e0 - 100, 0)), exp2_int(max(e1 - 100, 0)));
     big = __any_sync(0xffffffffu, e > 100);
   }
 };
@@ -416,6 +426,17 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
 // one slot and of V in the next. Item 2 i is task i's K, item 2 i + 1 its V; a
 // slot is refilled as soon as it has been used. A task is named by its place
 // among the cache's NT-tile units (-1: a block that is left out).
+template <int O, int END>
+__device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {  // END bytes from O on, 512 per step
+  if constexpr (O + 512 <= END) {
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;\n" ::"r"(dst), "l"(src), "n"(O));
+    copy_lines<O + 512, END>(dst, src);
+  } else if constexpr (O < END) {
+    if ((threadIdx.x & 31) * 16 < END - O)
+      asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;\n" ::"r"(dst), "l"(src), "n"(O));
+  }
+}
+
 template <int D, int NT>
 struct Ring {
   static constexpr int kParts = kTiles / NT;              // tasks of a block
@@ -428,9 +449,7 @@ struct Ring {
     const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(unit) * kSlotBytes + lane * 16;
     const uint32_t dst = smem_u32(ring) + (item & (kSlots - 1)) * kSlotBytes + lane * 16;
     if (ntok == NT * kTile) {
-#pragma unroll
-      for (int o = 0; o < kSlotBytes; o += 512)
-        if (kSlotBytes % 512 == 0 || o + lane * 16 < kSlotBytes) cp_async16(dst + o, src + o);
+      copy_lines<0, kSlotBytes>(dst, src);
     } else {  // the tiles that hold tokens
       const int bytes = (ntok + kTile - 1) / kTile * Fmt<D>::kTileBytes;
 #pragma unroll 1
@@ -492,83 +511,98 @@ __device__ __forceinline__ void run_tasks(const Kv4DecodeArgs& a, State<D>& st, 
 
 // The merge of a row's (or a split's) partials over CS CTAs. A warp's partial
 // is G x D normalised outputs in units of 4 channels, with the maximum and the
-// sum of every head. Unit u is merged by CTA u % CS: the warps store their
-// units straight into its shared memory, so that one cluster barrier is enough
-// and no CTA reads another's memory.
+// sum of every head. The units of the lanes g (channels 32 j + 4 g) are merged
+// by CTA g % CS: the warps store them straight into its shared memory, so that
+// one cluster barrier is enough and no CTA reads another's memory.
 template <int D>
 struct Merge {
-  int CS, rank, U;    // U units per CTA
-  unsigned magic;     // u / CS = u * magic >> 16 for u < 256
-  float4* o;          // [warp of the cluster][U]
-  float2* ml;         // [warp of the cluster][8 heads]
+  static constexpr int NG = D / kGroup;
+  int CS, rank, GS, U;  // GS lanes g and U = G · NG · GS units per CTA
+  float4* o;            // [warp of the cluster][head][group][lane g / CS]
+  float2* ml;           // [warp of the cluster][8 heads]
 
-  static __host__ __device__ int units(int G, int CS) { return (G * D / 4 + CS - 1) / CS; }
-  static __host__ __device__ int bytes(int G, int CS) { return CS * kWarps * (units(G, CS) * 16 + 64); }
+  static __host__ __device__ int lanes(int CS) { return (7 + CS) / CS; }
+  static __host__ __device__ int bytes(int G, int CS) { return CS * kWarps * (G * NG * lanes(CS) * 16 + 64); }
 
   __device__ __forceinline__ Merge(uint8_t* smem, int G, int CS, int rank)
-      : CS(CS), rank(rank), U(units(G, CS)), magic(65536u / unsigned(CS) + 1u), o(reinterpret_cast<float4*>(smem)),
+      : CS(CS), rank(rank), GS(lanes(CS)), U(G * NG * GS), o(reinterpret_cast<float4*>(smem)),
         ml(reinterpret_cast<float2*>(smem + CS * kWarps * U * 16)) {}
 
   template <bool CLUSTER>
-  __device__ __forceinline__ void push(const State<D>& st, int G) const {
-    constexpr int NG = D / kGroup;
+  __device__ __forceinline__ void push(State<D>& st, int G) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, from = rank * kWarps + int(threadIdx.x >> 5);
-    const float f = exp2f(float(int((st.lo & 0xffffu) >> 7) - 112));
+    // the minima's sums over the lanes g: lane g gets the total of one (group,
+    // head), and hands it to the others
+    float am[2 * NG];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) am[2 * j] = st.accm[j].x, am[2 * j + 1] = st.accm[j].y;
+#pragma unroll
+    for (int x = 16, n = NG; n >= 1; x >>= 1, n >>= 1) {
+      const bool up = (lane & x) != 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? am[i] : am[n + i], keep = up ? am[n + i] : am[i];
+        am[i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+      }
+    }
+    if (NG == 2) am[0] += __shfl_xor_sync(0xffffffffu, am[0], 4);
+    const int lo_e = int((st.lo & 0xffffu) >> 7);
+    float f = exp2_int(min(lo_e - 88, 127));  // 2^24 of the codes, 2^-112 of the two exponents' biases
+    if (lo_e > 215) {
+      f = exp2_int(lo_e - 112);
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.acc[j][0][e] *= 16777216.f, st.acc[j][1][e] *= 16777216.f;
+    }
+    const int slot = g / CS, owner = g - slot * CS;
+    float4* dst = o + from * U + 2 * t * NG * GS + slot;
+    if (CLUSTER) dst = cg::this_cluster().map_shared_rank(dst, owner);
     float l[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] = st.l[h];
 #pragma unroll
       for (int x = 4; x <= 16; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-      const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-      const int head = 2 * t + h;
+      const float inv = l[h] == 0.f ? 0.f : __fdividef(1.f, l[h]), f0 = inv * f, f1 = f0 * 0.0625f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        float am = h ? st.accm[j].y : st.accm[j].x;
-#pragma unroll
-        for (int x = 4; x <= 16; x <<= 1) am += __shfl_xor_sync(0xffffffffu, am, x);
-        am *= inv;
-        float4 v;
-        v.x = fmaf(st.acc[j][0][h] * (inv * 16777216.f), f, am);
-        v.y = fmaf(st.acc[j][0][2 + h] * (inv * 1048576.f), f, am);
-        v.z = fmaf(st.acc[j][1][h] * (inv * 16777216.f), f, am);
-        v.w = fmaf(st.acc[j][1][2 + h] * (inv * 1048576.f), f, am);
-        if (head < G) {
-          const int u = head * (D / 4) + 8 * j + g, slot = int(unsigned(u) * magic >> 16), owner = u - slot * CS;
-          float4* dst = o + from * U + slot;
-          if (CLUSTER) dst = cg::this_cluster().map_shared_rank(dst, owner);
-          *dst = v;
-        }
+        const int from_g = NG == 4 ? 2 * j + h : 2 * (2 * j + h);
+        const float m = __shfl_sync(0xffffffffu, am[0], from_g * 4 + t) * inv;
+        if (2 * t + h < G)
+          dst[(h * NG + j) * GS] = make_float4(fmaf(st.acc[j][0][h], f0, m), fmaf(st.acc[j][0][2 + h], f1, m),
+                                               fmaf(st.acc[j][1][h], f0, m), fmaf(st.acc[j][1][2 + h], f1, m));
       }
     }
     if (g < CS) {
-      float4* dst = reinterpret_cast<float4*>(ml + from * 8 + 2 * t);
-      if (CLUSTER) dst = cg::this_cluster().map_shared_rank(dst, g);
-      *dst = make_float4(st.m[0], l[0], st.m[1], l[1]);
+      float4* to = reinterpret_cast<float4*>(ml + from * 8 + 2 * t);
+      if (CLUSTER) to = cg::this_cluster().map_shared_rank(to, g);
+      *to = make_float4(st.m[0], l[0], st.m[1], l[1]);
     }
   }
 
-  // Eight lanes to a unit; out(head, channel, outputs, lse) stores it. A row
+  // LANES lanes to a unit; out(head, channel, outputs, lse) stores it. A row
   // whose sum is NaN in any partial is NaN.
-  template <typename Out>
-  __device__ __forceinline__ void run(int G, Out out) const {
-    const int sub = threadIdx.x & 7, n = CS * kWarps;
-    for (int base = 0; base < U; base += kThreads / 8) {
-      const int s = base + int(threadIdx.x >> 3), u = s * CS + rank;
-      const bool live = s < U && u < G * D / 4;
-      const int head = live ? u / (D / 4) : 0;
+  template <int LANES, typename Out>
+  __device__ __forceinline__ void run(Out out) const {
+    const int sub = threadIdx.x & (LANES - 1), n = CS * kWarps;
+    for (int base = 0; base < U; base += kThreads / LANES) {
+      const int s = min(base + int(threadIdx.x) / LANES, U - 1), hj = s / GS, g = (s - hj * GS) * CS + rank;
+      const int head = hj / NG;
+      const float2* mh = ml + head;
+      const float4* oh = o + s;
       float M = -INFINITY;
-      for (int w = sub; w < n; w += 8) M = fmaxf(M, ml[w * 8 + head].x);
+      for (int w = sub; w < n; w += LANES) M = fmaxf(M, mh[w * 8].x);
 #pragma unroll
-      for (int x = 1; x <= 4; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      for (int x = 1; x < LANES; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
       const float ref = M == -INFINITY ? 0.f : M;
       float den = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = sub; w < n; w += 8) {
-        const float2 p = ml[w * 8 + head];
+      for (int w = sub; w < n; w += LANES) {
+        const float2 p = mh[w * 8];
         if (p.y == 0.f) continue;  // a warp without tokens
-        const float k = p.y * exp2f(p.x - ref);
-        const float4 y = o[w * U + (live ? s : 0)];
+        const float k = p.y * exp2_approx(p.x - ref);
+        const float4 y = oh[w * U];
         den += k;
         v.x = fmaf(k, y.x, v.x);
         v.y = fmaf(k, y.y, v.y);
@@ -576,16 +610,16 @@ struct Merge {
         v.w = fmaf(k, y.w, v.w);
       }
 #pragma unroll
-      for (int x = 1; x <= 4; x <<= 1) {
+      for (int x = 1; x < LANES; x <<= 1) {
         den += __shfl_xor_sync(0xffffffffu, den, x);
         v.x += __shfl_xor_sync(0xffffffffu, v.x, x);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, x);
         v.z += __shfl_xor_sync(0xffffffffu, v.z, x);
         v.w += __shfl_xor_sync(0xffffffffu, v.w, x);
       }
-      if (!live || sub != 0) continue;
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      out(head, 4 * (u % (D / 4)), make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv),
+      if (sub != 0 || g >= 8 || base + int(threadIdx.x) / LANES >= U) continue;
+      const float inv = den == 0.f ? 0.f : __fdividef(1.f, den);
+      out(head, 32 * (hj - head * NG) + 4 * g, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv),
           den == 0.f ? -INFINITY : (M + log2f(den) - kPShift) * kLn2);
     }
   }
@@ -764,36 +798,43 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
     mg.template push<false>(st, a.G);
     __syncthreads();
   }
-  mg.run(a.G, [&](int head, int col, float4 o, float lse) {
+  mg.template run<CLUSTER ? 8 : 4>([&](int head, int col, float4 o, float lse) {
     const size_t row = (size_t(bh) * a.G + head) * a.n_split + split;
     *reinterpret_cast<float4*>(a.o_part + row * D + col) = o;
     if (col == 0) a.lse_part[row] = lse;
   });
 }
 
-// One cluster per (sequence, KV head). Every warp selects the row's blocks
-// itself, in registers, and takes every W-th task of the list [current block,
-// picks...]: there is no block-wide barrier before the merge, and the
-// redundant selection is cheaper than a hand-over.
+// One cluster per (sequence, KV head). In each CTA one warp selects the row's
+// blocks, in registers, and another takes the row's LSE if it is needed; then
+// every warp of the cluster takes every W-th task of the list [current block,
+// picks...]. The CTAs' redundant selection is cheaper than a hand-over between
+// them, a selection by every warp was not: three CTAs share a multiprocessor,
+// and their instructions are what bounds the step.
 template <int D, int NT, int CAP>
 __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
   using R = Ring<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sel_s[kWarps][kMaxPicks + 1];
+  __shared__ int sel_s[kMaxPicks + 1];
   __shared__ int unit_s[kWarps][kWarpTasks];
   __shared__ float lam_s[kWarps][kWarpTasks];
+  __shared__ float lse_s;
   const int CS = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps, worker = warp * CS + rank;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps;
+  // the selecting warp is the last: the first ones start on the current block
+  const int worker = warp * CS + rank;
   const int bh = int(blockIdx.x) / CS, b = bh / a.Hkv, h = bh % a.Hkv;
   const int NB = a.Lmax / kBlock;
   uint8_t* ring = smem + warp * R::kBytes;
   const float* srow = a.s + size_t(bh) * NB;
+  const bool soft = a.gate == SAS_GATE_LOG_SOFTMAX || a.gate == SAS_GATE_SOFTMAX_OUTSIDE;
   cluster_begin();
   griddep_launch_dependents();
   griddep_wait();
   int L = a.cache_len[b];
   Row<CAP> row;
-  row.read(srow, NB);
+  const bool selects = warp == kWarps - 1, sums = warp == kWarps - 2 && (soft || (rank == 0 && a.lse_s_out != nullptr));
+  if (selects || sums) row.read(srow, NB);
   uint4 raw[D / kGroup];
   Query<D>::read(a.q + size_t(bh) * a.G * D, a.G, raw);
   if (a.c.table != nullptr && tid * 32 < NB)  // the row's pages, for the lookup of the picks
@@ -815,35 +856,34 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
       cp_async_commit();
     }
   }
-  row.make(c);
-  row.select(c, n_pick, sel_s[warp]);
-  __syncwarp();
+  if (selects) {
+    row.make(c);
+    row.select(c, n_pick, sel_s);
+  } else if (sums) {
+    row.make(c);
+    const float lse = row.lse(c);
+    if (lane == 0) {
+      lse_s = lse;
+      if (rank == 0 && a.lse_s_out != nullptr) a.lse_s_out[bh] = lse;
+    }
+  }
+  Query<D> q;
+  if (!selects) q.make(raw, a.scale);
+  __syncthreads();  // the picks and the LSE
+  const float lse = soft ? lse_s : 0.f;
   for (int k = lane; k < n; k += 32) {
     const int task = k * W + worker, pos = task / R::kParts;
-    const int m = pos > 0 ? sel_s[warp][pos - 1] : c;
+    const int m = pos > 0 ? sel_s[pos - 1] : c;
+    const float sm = a.gated && pos > 0 ? __ldg(srow + m) : 0.f;
     const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
     unit_s[warp][k] = rec < 0 ? -1 : rec * R::kParts + task % R::kParts;
-    if (a.gated) lam_s[warp][k] = rec < 0 || pos == 0 ? 0.f : __ldg(srow + m);
+    lam_s[warp][k] = a.gated && pos > 0 && rec >= 0 ? gate_lam2(a.gate, sm, lse) : 0.f;
   }
   __syncwarp();
   R::fill(ring, a.c, unit_s[warp], n, ntok0, has_cur ? 2 : 0);
-  // while the records are on their way: the queries, the gates and the row's outputs
-  Query<D> q;
-  q.make(raw, a.scale);
-  const bool first = rank == 0 && warp == 0;
-  const bool soft = a.gate == SAS_GATE_LOG_SOFTMAX || a.gate == SAS_GATE_SOFTMAX_OUTSIDE;
-  float lse = 0.f;
-  if (soft || (first && a.lse_s_out != nullptr)) lse = row.lse(c);
-  if (a.gated) {
-    for (int k = lane; k < n; k += 32)
-      if (unit_s[warp][k] >= 0 && (k > 0 || !has_cur)) lam_s[warp][k] = gate_lam2(a.gate, lam_s[warp][k], lse);
-    __syncwarp();
-  }
-  if (first) {
-    if (a.lse_s_out != nullptr && lane == 0) a.lse_s_out[bh] = lse;
-    if (a.idx_out != nullptr)
-      for (int i = lane; i < a.K; i += 32) a.idx_out[size_t(bh) * a.K + i] = i < n_pick ? sel_s[warp][i] : -1;
-  }
+  if (selects) q.make(raw, a.scale);
+  if (rank == 0 && warp == 0 && a.idx_out != nullptr)
+    for (int i = lane; i < a.K; i += 32) a.idx_out[size_t(bh) * a.K + i] = i < n_pick ? sel_s[i] : -1;
   State<D> st;
   st.clear();
   run_tasks<D, NT>(a, st, q, ring, unit_s[warp], lam_s[warp], n, ntok0);
@@ -851,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
   cluster_begun();
   mg.template push<true>(st, a.G);
   cluster_sync();
-  mg.run(a.G, [&](int head, int col, float4 o, float ls) {
+  mg.template run<8>([&](int head, int col, float4 o, float ls) {
     const size_t at = size_t(bh) * a.G + head;
     *reinterpret_cast<uint2*>(a.o + at * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     if (col == 0 && a.lse_o != nullptr) a.lse_o[at] = ls;
