@@ -581,46 +581,53 @@ struct Merge {
     }
   }
 
-  // LANES lanes to a unit; out(head, channel, outputs, lse) stores it. A row
-  // whose sum is NaN in any partial is NaN.
-  template <int LANES, typename Out>
+  // As many lanes to a unit (1 to 8) as the CTA has; out(head, channel, outputs,
+  // lse) stores it. A row whose sum is NaN in any partial is NaN. The loops are
+  // not unrolled: the code runs once, and fetching it is part of its time.
+  template <typename Out>
   __device__ __forceinline__ void run(Out out) const {
-    const int sub = threadIdx.x & (LANES - 1), n = CS * kWarps;
-    for (int base = 0; base < U; base += kThreads / LANES) {
-      const int s = min(base + int(threadIdx.x) / LANES, U - 1), hj = s / GS, g = (s - hj * GS) * CS + rank;
+    const int n = CS * kWarps;
+    int lanes = 8;
+    while (lanes > 1 && lanes * U > kThreads) lanes >>= 1;
+    const int sub = threadIdx.x & (lanes - 1), unit = int(threadIdx.x) / lanes, step = kThreads / lanes;
+#pragma unroll 1
+    for (int base = 0; base < U; base += step) {
+      const int s = min(base + unit, U - 1), hj = s / GS, g = (s - hj * GS) * CS + rank;
       const int head = hj / NG;
       const float2* mh = ml + head;
       const float4* oh = o + s;
       float M = -INFINITY;
-      for (int w = sub; w < n; w += LANES) M = fmaxf(M, mh[w * 8].x);
-#pragma unroll
-      for (int x = 1; x < LANES; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+#pragma unroll 1
+      for (int w = sub; w < n; w += lanes) M = fmaxf(M, mh[w * 8].x);
+#pragma unroll 1
+      for (int x = 1; x < lanes; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
       const float ref = M == -INFINITY ? 0.f : M;
       float den = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = sub; w < n; w += LANES) {
+#pragma unroll 1
+      for (int w = sub; w < n; w += lanes) {
         const float2 p = mh[w * 8];
-        if (p.y == 0.f) continue;  // a warp without tokens
-        const float k = p.y * exp2_approx(p.x - ref);
         const float4 y = oh[w * U];
-        den += k;
-        v.x = fmaf(k, y.x, v.x);
-        v.y = fmaf(k, y.y, v.y);
-        v.z = fmaf(k, y.z, v.z);
-        v.w = fmaf(k, y.w, v.w);
+        const float k = p.y * exp2_approx(p.x - ref);
+        const bool any = p.y != 0.f;  // not a warp without tokens
+        den += any ? k : 0.f;
+        v.x = any ? fmaf(k, y.x, v.x) : v.x;
+        v.y = any ? fmaf(k, y.y, v.y) : v.y;
+        v.z = any ? fmaf(k, y.z, v.z) : v.z;
+        v.w = any ? fmaf(k, y.w, v.w) : v.w;
       }
-#pragma unroll
-      for (int x = 1; x < LANES; x <<= 1) {
+#pragma unroll 1
+      for (int x = 1; x < lanes; x <<= 1) {
         den += __shfl_xor_sync(0xffffffffu, den, x);
         v.x += __shfl_xor_sync(0xffffffffu, v.x, x);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, x);
         v.z += __shfl_xor_sync(0xffffffffu, v.z, x);
         v.w += __shfl_xor_sync(0xffffffffu, v.w, x);
       }
-      if (sub != 0 || g >= 8 || base + int(threadIdx.x) / LANES >= U) continue;
+      if (sub != 0 || g >= 8 || base + unit >= U) continue;
       const float inv = den == 0.f ? 0.f : __fdividef(1.f, den);
       out(head, 32 * (hj - head * NG) + 4 * g, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv),
-          den == 0.f ? -INFINITY : (M + log2f(den) - kPShift) * kLn2);
+          den == 0.f ? -INFINITY : (M + __log2f(den) - kPShift) * kLn2);
     }
   }
 };
@@ -641,9 +648,10 @@ __device__ __forceinline__ float key_score(uint32_t k) {
 // One warp's Top-K of a score row, without a block-wide barrier: lane i holds
 // the keys of blocks i, 32 + i, ... in registers. A bisection between the
 // smallest and the largest key finds a threshold with n keys at or above it, in
-// a dozen counts of the row: at first it halves the range of values, which
-// spread evenly over their own range, and after 16 steps that of keys, which
-// ends for sure. Where a tie is cut, it ends on the tied key.
+// half a dozen counts of the row: each step quarters the range, at first that
+// of the values, which spread evenly over their own range, and after 8 steps
+// that of the keys, which ends for sure. Where a tie is cut, it ends on the
+// tied key.
 template <int CAP>
 struct Row {
   uint32_t key[CAP];  // orderable key + 1, 0 past the history
@@ -686,6 +694,7 @@ struct Row {
       for (int i = 0; i < CAP; ++i) lo = min(lo, key[i] - 1u);
       lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
       int above = 0;  // count(hi)
+#pragma unroll 1
       for (int round = 0;; ++round) {
         if (hi - lo <= 1u) {
           thr = hi;
@@ -693,26 +702,40 @@ struct Row {
           need = n - above;
           break;
         }
-        uint32_t mid = lo + (hi - lo) / 2u;
-        if (round < 16) {
-          const uint32_t v = score_key(0.5f * key_score(lo - 1u) + 0.5f * key_score(hi - 1u)) + 1u;
-          if (v > lo && v < hi) mid = v;
+        // three keys in (lo, hi), in ascending order (equal ones do no harm)
+        uint32_t mid[3];
+        const float vl = key_score(lo - 1u), vh = key_score(hi - 1u);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          const uint32_t even = lo + 1u + uint32_t((uint64_t(hi - lo - 1u) * (u + 1)) >> 2);
+          const uint32_t v = score_key(fmaf(vh, 0.25f * (u + 1), vl * (0.75f - 0.25f * u))) + 1u;
+          mid[u] = round < 8 && v > lo && v < hi ? v : min(even, hi - 1u);
         }
-        int cnt = 0;
+        mid[1] = max(mid[1], mid[0]);
+        mid[2] = max(mid[2], mid[1]);
+        int cnt[3] = {0, 0, 0};
 #pragma unroll
         for (int i = 0; i < CAP; ++i)
-          if (CAP <= 16 || 32 * i < c) cnt += key[i] >= mid ? 1 : 0;
-        cnt = __reduce_add_sync(0xffffffffu, cnt);
-        if (cnt == n) {
-          thr = mid;
+          if (CAP <= 16 || 32 * i < c) {
+#pragma unroll
+            for (int u = 0; u < 3; ++u) cnt[u] += key[i] >= mid[u] ? 1 : 0;
+          }
+#pragma unroll
+        for (int u = 0; u < 3; ++u) cnt[u] = __reduce_add_sync(0xffffffffu, cnt[u]);
+        const int at = cnt[0] == n ? 0 : cnt[1] == n ? 1 : 2;
+        if (cnt[at] == n) {
+          thr = mid[at];
           break;
         }
-        if (cnt > n) {
-          lo = mid;
-        } else {
-          hi = mid;
-          above = cnt;
-        }
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+          if (cnt[u] > n) lo = mid[u];
+#pragma unroll
+        for (int u = 2; u >= 0; --u)
+          if (cnt[u] < n) {
+            hi = mid[u];
+            above = cnt[u];
+          }
       }
     }
     const unsigned below = (1u << lane) - 1u;
@@ -798,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
     mg.template push<false>(st, a.G);
     __syncthreads();
   }
-  mg.template run<CLUSTER ? 8 : 4>([&](int head, int col, float4 o, float lse) {
+  mg.run([&](int head, int col, float4 o, float lse) {
     const size_t row = (size_t(bh) * a.G + head) * a.n_split + split;
     *reinterpret_cast<float4*>(a.o_part + row * D + col) = o;
     if (col == 0) a.lse_part[row] = lse;
@@ -891,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
   cluster_begun();
   mg.template push<true>(st, a.G);
   cluster_sync();
-  mg.template run<8>([&](int head, int col, float4 o, float ls) {
+  mg.run([&](int head, int col, float4 o, float ls) {
     const size_t at = size_t(bh) * a.G + head;
     *reinterpret_cast<uint2*>(a.o + at * D + col) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     if (col == 0 && a.lse_o != nullptr) a.lse_o[at] = ls;
@@ -949,7 +972,7 @@ static cudaError_t multiprocessors(int* sms) {
 
 #ifndef KV4_NT_SPLIT
 #define KV4_NT_SPLIT 4
-#define KV4_NT_FUSED 2
+#define KV4_NT_FUSED 4
 #endif
 
 // Split form. The cluster size: the largest power of two that keeps every CTA
