@@ -40,7 +40,7 @@ constexpr int kWarps = 4;           // warps of a CTA
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;      // portable cluster size
 constexpr int kMaxPicks = 255;      // one-launch form: picks of a row
-constexpr int kWarpTasks = 128;     // tasks of a warp: 256 blocks in halves over the 4 warps of one CTA
+constexpr int kWarpBlocks = 64;     // blocks of a warp: a row's 256 over the 4 warps of one CTA
 constexpr float kPShift = 8.f;      // P is kept times 2^8
 constexpr int kStepField = 17;      // exponent field that the largest step gets in fp16 when the base is set
 constexpr int kStepLimit = 23;      // a step with this field (2^8) moves the base: P·s stays under 2^16
@@ -422,10 +422,9 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
   }
 }
 
-// A warp's ring: tasks of NT tiles (a block, or half of one), NT tiles of K in
-// one slot and of V in the next. Item 2 i is task i's K, item 2 i + 1 its V; a
-// slot is refilled as soon as it has been used. A task is named by its place
-// among the cache's NT-tile units (-1: a block that is left out).
+// A warp's ring: the K record of a block in one slot, its V record in the other.
+// Item 2 i is block i's K, item 2 i + 1 its V; a slot is refilled as soon as it
+// has been used. Records are named by their number (-1: a block left out).
 template <int O, int END>
 __device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {  // END bytes from O on, 512 per step
   if constexpr (O + 512 <= END) {
@@ -437,74 +436,83 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {  
   }
 }
 
-template <int D, int NT>
+template <int D>
 struct Ring {
-  static constexpr int kParts = kTiles / NT;              // tasks of a block
-  static constexpr int kSlots = 2 * kParts;               // a block's K and V in all
-  static constexpr int kSlotBytes = NT * Fmt<D>::kTileBytes;
-  static constexpr int kBytes = kSlots * kSlotBytes;
+  static constexpr int kRecord = Fmt<D>::kRecord;
+  static constexpr int kBytes = 2 * kRecord;
 
-  static __device__ __forceinline__ void issue(uint8_t* ring, const Cache& c, int item, int unit, int ntok) {
+  static __device__ __forceinline__ void issue(uint8_t* ring, const Cache& c, int item, int rec, int ntok) {
     const int lane = threadIdx.x & 31;
-    const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(unit) * kSlotBytes + lane * 16;
-    const uint32_t dst = smem_u32(ring) + (item & (kSlots - 1)) * kSlotBytes + lane * 16;
-    if (ntok == NT * kTile) {
-      copy_lines<0, kSlotBytes>(dst, src);
+    const uint8_t* src = ((item & 1) ? c.v : c.k) + size_t(rec) * kRecord + lane * 16;
+    const uint32_t dst = smem_u32(ring) + (item & 1) * kRecord + lane * 16;
+    if (ntok == kBlock) {
+      copy_lines<0, kRecord>(dst, src);
     } else {  // the tiles that hold tokens
       const int bytes = (ntok + kTile - 1) / kTile * Fmt<D>::kTileBytes;
 #pragma unroll 1
       for (int o = 0; o + lane * 16 < bytes; o += 512) cp_async16(dst + o, src + o);
     }
   }
-  // Items from `item` on, up to a full ring, each its own copy group.
-  static __device__ __forceinline__ void fill(uint8_t* ring, const Cache& c, const int* unit_s, int n, int ntok0, int item) {
-    for (; item < kSlots; ++item) step(ring, c, unit_s, n, ntok0, item);
-  }
-  static __device__ __forceinline__ void step(uint8_t* ring, const Cache& c, const int* unit_s, int n, int ntok0, int item) {
+  // Item `item` of n blocks, as a copy group of its own.
+  static __device__ __forceinline__ void step(uint8_t* ring, const Cache& c, const int* rec_s, int n, int ntok0, int item) {
     if (item < 2 * n) {
-      const int unit = unit_s[item >> 1];
-      if (unit >= 0) issue(ring, c, item, unit, item < 2 ? ntok0 : NT * kTile);
+      const int rec = rec_s[item >> 1];
+      if (rec >= 0) issue(ring, c, item, rec, item < 2 ? ntok0 : kBlock);
     }
     cp_async_commit();
   }
 };
 
-// A warp over its n tasks: units unit_s, gates lam_s (log2). The first task has
-// ntok0 tokens, the others all. The ring has been filled.
-template <int D, int NT>
-__device__ __forceinline__ void run_tasks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
-                                          const int* unit_s, const float* lam_s, int n, int ntok0) {
-  using R = Ring<D, NT>;
+__device__ __forceinline__ void weigh(float2& p, float w) {
+  p.x *= w;
+  p.y *= w;
+}
+
+// A warp over its n blocks: records rec_s, gates lam_s (log2). The first block
+// has ntok0 tokens, the others all. Both items of the first are under way. A
+// block that is not full goes through a loop of single tiles, which keeps the
+// code that a warp has to fetch small.
+template <int D>
+__device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
+                                           const int* rec_s, const float* lam_s, int n, int ntok0) {
+  using R = Ring<D>;
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int ntok = unit_s[i] < 0 ? 0 : i == 0 ? ntok0 : NT * kTile;
-    const float lam = a.gated ? lam_s[i] : 0.f;
-    float2 S[NT][2];
-    cp_async_wait<R::kSlots - 1>();
-    __syncwarp();
-    const uint8_t* rec = ring + (2 * i & (R::kSlots - 1)) * R::kSlotBytes;
-    if (ntok == NT * kTile)
-      score_block<D, NT, true>(rec, q, ntok, S);
-    else
-      score_block<D, NT, false>(rec, q, ntok, S);
-    __syncwarp();
-    R::step(ring, a.c, unit_s, n, ntok0, 2 * i + R::kSlots);
-    softmax_block<D, NT>(st, q, a.outside ? 0.f : lam, S);
-    if (a.outside) {
-      const float gw = exp2f(lam);
+    const int ntok = rec_s[i] < 0 ? 0 : i == 0 ? ntok0 : kBlock;
+    const float lam = a.gated ? lam_s[i] : 0.f, bias = a.outside ? 0.f : lam;
+    if (ntok == kBlock) {
+      float2 S[kTiles][2];
+      cp_async_wait<1>();
+      __syncwarp();
+      score_block<D, kTiles, true>(ring, q, ntok, S);
+      __syncwarp();
+      R::step(ring, a.c, rec_s, n, ntok0, 2 * i + 2);
+      softmax_block<D, kTiles>(st, q, bias, S);
+      if (a.outside) {
+        const float gw = exp2f(lam);
 #pragma unroll
-      for (int k = 0; k < NT; ++k)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) S[k][u] = make_float2(S[k][u].x * gw, S[k][u].y * gw);
+        for (int k = 0; k < kTiles; ++k) weigh(S[k][0], gw), weigh(S[k][1], gw);
+      }
+      cp_async_wait<1>();
+      __syncwarp();
+      value_block<D, kTiles, true>(ring + R::kRecord, st, ntok, S);
+    } else {
+      cp_async_wait<0>();
+      __syncwarp();
+#pragma unroll 1
+      for (int k = 0; k * kTile < ntok; ++k) {
+        float2 S[1][2];
+        const uint8_t* tile = ring + k * Fmt<D>::kTileBytes;
+        score_block<D, 1, false>(tile, q, ntok - k * kTile, S);
+        softmax_block<D, 1>(st, q, bias, S);
+        if (a.outside) weigh(S[0][0], exp2f(lam)), weigh(S[0][1], exp2f(lam));
+        value_block<D, 1, false>(tile + R::kRecord, st, ntok - k * kTile, S);
+      }
+      __syncwarp();
+      R::step(ring, a.c, rec_s, n, ntok0, 2 * i + 2);
     }
-    cp_async_wait<R::kSlots - 1>();
     __syncwarp();
-    rec += R::kSlotBytes;  // the number of slots is even
-    if (ntok == NT * kTile)
-      value_block<D, NT, true>(rec, st, ntok, S);
-    else
-      value_block<D, NT, false>(rec, st, ntok, S);
-    __syncwarp();
-    R::step(ring, a.c, unit_s, n, ntok0, 2 * i + 1 + R::kSlots);
+    R::step(ring, a.c, rec_s, n, ntok0, 2 * i + 3);
   }
   cp_async_wait<0>();
 }
@@ -722,9 +730,8 @@ struct Row {
           }
 #pragma unroll
         for (int u = 0; u < 3; ++u) cnt[u] = __reduce_add_sync(0xffffffffu, cnt[u]);
-        const int at = cnt[0] == n ? 0 : cnt[1] == n ? 1 : 2;
-        if (cnt[at] == n) {
-          thr = mid[at];
+        if (cnt[0] == n || cnt[1] == n || cnt[2] == n) {
+          thr = cnt[0] == n ? mid[0] : cnt[1] == n ? mid[1] : mid[2];
           break;
         }
 #pragma unroll
@@ -740,15 +747,20 @@ struct Row {
     }
     const unsigned below = (1u << lane) - 1u;
     int base = 0;
+    if (need == 0) {
+#pragma unroll
+      for (int i = 0; i < CAP; ++i) {
+        const unsigned b = __ballot_sync(0xffffffffu, key[i] >= thr);
+        if (key[i] >= thr) sel[base + __popc(b & below)] = 32 * i + lane;
+        base += __popc(b);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < CAP; ++i) {
-      if (32 * i >= c) break;
-      bool take = key[i] >= thr;
-      if (need > 0) {
-        const unsigned eq = __ballot_sync(0xffffffffu, key[i] == tied);
-        take = take || (key[i] == tied && __popc(eq & below) < need);
-        need -= min(need, __popc(eq));
-      }
+      const unsigned eq = __ballot_sync(0xffffffffu, key[i] == tied);
+      const bool take = key[i] >= thr || (key[i] == tied && __popc(eq & below) < need);
+      need -= min(need, __popc(eq));
       const unsigned b = __ballot_sync(0xffffffffu, take);
       if (take) sel[base + __popc(b & below)] = 32 * i + lane;
       base += __popc(b);
@@ -758,14 +770,14 @@ struct Row {
 
 }  // namespace
 
-// One CTA per (sequence, KV head, split), or a cluster of CS. The tasks of the
-// split's run go round the cluster's warps.
-template <int D, int NT, bool CLUSTER>
+// One CTA per (sequence, KV head, split), or a cluster of CS. The blocks of
+// the split's run go round the cluster's warps.
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4DecodeArgs a) {
-  using R = Ring<D, NT>;
+  using R = Ring<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int unit_s[kWarps][kMaxDecodeBlocksPerSplit * R::kParts / kWarps];
-  __shared__ float lam_s[kWarps][kMaxDecodeBlocksPerSplit * R::kParts / kWarps];
+  __shared__ int rec_s[kWarps][kMaxDecodeBlocksPerSplit / kWarps];
+  __shared__ float lam_s[kWarps][kMaxDecodeBlocksPerSplit / kWarps];
   const int CS = CLUSTER ? int(cg::this_cluster().num_blocks()) : 1;
   const int rank = CLUSTER ? int(cg::this_cluster().block_rank()) : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps, worker = warp * CS + rank;
@@ -784,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
   }
   const int c = (L - 1) / kBlock, nl = 1 + min(a.K, c);
   const int per = (nl + a.n_split - 1) / a.n_split;
-  const int lo = min(split * per, nl), tasks = (min(lo + per, nl) - lo) * R::kParts;
-  const int n = worker < tasks ? (tasks - 1 - worker) / W + 1 : 0;
+  const int lo = min(split * per, nl), blocks = min(lo + per, nl) - lo;
+  const int n = worker < blocks ? (blocks - 1 - worker) / W + 1 : 0;
   for (int k = lane; k < n; k += 32) {
-    const int task = k * W + worker, pos = lo + task / R::kParts;
+    const int pos = lo + k * W + worker;
     int m = c;
     float lam = 0.f;
     if (pos > 0) {
@@ -799,18 +811,18 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
         lam = gate_lam2(a.gate, a.s[size_t(bh) * NB + m], a.lse_s_in != nullptr ? a.lse_s_in[bh] : 0.f);
     }
     const int rec = m < 0 ? -1 : record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-    unit_s[warp][k] = rec < 0 ? -1 : rec * R::kParts + task % R::kParts;
+    rec_s[warp][k] = rec;
     lam_s[warp][k] = rec < 0 ? 0.f : lam;
   }
   __syncwarp();
-  // tokens of the first task: the current block's, if it is one of its parts
-  const int ntok0 = lo == 0 && worker < R::kParts ? max(0, min(NT * kTile, L - c * kBlock - worker * NT * kTile)) : NT * kTile;
-  R::fill(ring, a.c, unit_s[warp], n, ntok0, 0);
+  const int ntok0 = lo == 0 && worker == 0 ? L - c * kBlock : kBlock;  // tokens of the warp's first block
+  R::step(ring, a.c, rec_s[warp], n, ntok0, 0);
+  R::step(ring, a.c, rec_s[warp], n, ntok0, 1);
   Query<D> q;
   q.make(raw, a.scale);
   State<D> st;
   st.clear();
-  run_tasks<D, NT>(a, st, q, ring, unit_s[warp], lam_s[warp], n, ntok0);
+  run_blocks<D>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
   const Merge<D> mg(CLUSTER ? smem + kWarps * R::kBytes : smem, a.G, CS, rank);
   if (CLUSTER) {
     cluster_begun();
@@ -830,17 +842,17 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
 
 // One cluster per (sequence, KV head). In each CTA one warp selects the row's
 // blocks, in registers, and another takes the row's LSE if it is needed; then
-// every warp of the cluster takes every W-th task of the list [current block,
+// every warp of the cluster takes every W-th block of the list [current block,
 // picks...]. The CTAs' redundant selection is cheaper than a hand-over between
 // them, a selection by every warp was not: three CTAs share a multiprocessor,
 // and their instructions are what bounds the step.
-template <int D, int NT, int CAP>
+template <int D, int CAP>
 __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
-  using R = Ring<D, NT>;
+  using R = Ring<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int sel_s[kMaxPicks + 1];
-  __shared__ int unit_s[kWarps][kWarpTasks];
-  __shared__ float lam_s[kWarps][kWarpTasks];
+  __shared__ int rec_s[kWarps][kWarpBlocks];
+  __shared__ float lam_s[kWarps][kWarpBlocks];
   __shared__ float lse_s;
   const int CS = int(cg::this_cluster().num_blocks()), rank = int(cg::this_cluster().block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = CS * kWarps;
@@ -866,16 +878,15 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
     if (tid == 0) raise_error(a.err, SAS_ERR_DEVICE_INDEX);
     L = max(1, min(L, a.Lmax));
   }
-  const int c = (L - 1) / kBlock, n_pick = min(a.K, c), tasks = (1 + n_pick) * R::kParts;
-  const int n = worker < tasks ? (tasks - 1 - worker) / W + 1 : 0;
-  const bool has_cur = worker < R::kParts;
-  const int ntok0 = has_cur ? max(0, min(NT * kTile, L - c * kBlock - worker * NT * kTile)) : NT * kTile;
+  const int c = (L - 1) / kBlock, n_pick = min(a.K, c);
+  const int n = worker <= n_pick ? (n_pick - worker) / W + 1 : 0;
+  const bool has_cur = worker == 0;
+  const int ntok0 = has_cur ? L - c * kBlock : kBlock;
   if (has_cur) {  // the current block needs no selection
     const int rec = record_of(a.c, b, h, c, a.Hkv, NB, a.err);
-    const int unit = rec < 0 ? -1 : rec * R::kParts + worker;
 #pragma unroll
     for (int item = 0; item < 2; ++item) {
-      if (unit >= 0) R::issue(ring, a.c, item, unit, ntok0);
+      if (rec >= 0) R::issue(ring, a.c, item, rec, ntok0);
       cp_async_commit();
     }
   }
@@ -895,21 +906,23 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
   __syncthreads();  // the picks and the LSE
   const float lse = soft ? lse_s : 0.f;
   for (int k = lane; k < n; k += 32) {
-    const int task = k * W + worker, pos = task / R::kParts;
-    const int m = pos > 0 ? sel_s[pos - 1] : c;
+    const int pos = k * W + worker, m = pos > 0 ? sel_s[pos - 1] : c;
     const float sm = a.gated && pos > 0 ? __ldg(srow + m) : 0.f;
     const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-    unit_s[warp][k] = rec < 0 ? -1 : rec * R::kParts + task % R::kParts;
+    rec_s[warp][k] = rec;
     lam_s[warp][k] = a.gated && pos > 0 && rec >= 0 ? gate_lam2(a.gate, sm, lse) : 0.f;
   }
   __syncwarp();
-  R::fill(ring, a.c, unit_s[warp], n, ntok0, has_cur ? 2 : 0);
+  if (!has_cur) {
+    R::step(ring, a.c, rec_s[warp], n, ntok0, 0);
+    R::step(ring, a.c, rec_s[warp], n, ntok0, 1);
+  }
   if (selects) q.make(raw, a.scale);
   if (rank == 0 && warp == 0 && a.idx_out != nullptr)
     for (int i = lane; i < a.K; i += 32) a.idx_out[size_t(bh) * a.K + i] = i < n_pick ? sel_s[i] : -1;
   State<D> st;
   st.clear();
-  run_tasks<D, NT>(a, st, q, ring, unit_s[warp], lam_s[warp], n, ntok0);
+  run_blocks<D>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
   const Merge<D> mg(smem + kWarps * R::kBytes, a.G, CS, rank);
   cluster_begun();
   mg.template push<true>(st, a.G);
@@ -970,17 +983,12 @@ static cudaError_t multiprocessors(int* sms) {
   return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
-#ifndef KV4_NT_SPLIT
-#define KV4_NT_SPLIT 4
-#define KV4_NT_FUSED 4
-#endif
-
 // Split form. The cluster size: the largest power of two that keeps every CTA
 // resident at once (16 warps per SM), at most 8 and at most one warp per block
 // of a split.
 template <int D>
 static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int NT = KV4_NT_SPLIT, ring = kWarps * Ring<D, NT>::kBytes;
+  constexpr int ring = kWarps * Ring<D>::kBytes;
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
@@ -988,8 +996,8 @@ static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
   const int want = min(min(kMaxCluster, (per + kWarps - 1) / kWarps), sms * 4 / items);
   int cs = 1;
   while (cs * 2 <= want) cs *= 2;
-  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, NT, false>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
-  return launch_ctas(kv4_decode_split_kernel<D, NT, true>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, false>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
+  return launch_ctas(kv4_decode_split_kernel<D, true>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
 }
 
 cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl, const float* s,
@@ -1005,16 +1013,16 @@ cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c
 }
 
 // One launch. The cluster size: as many CTAs per row as keep the grid in one
-// wave of resident CTAs, at most 8 and at most one warp per task of the list.
+// wave of resident CTAs, at most 8 and at most one warp per block of the list.
 template <int D, int CAP>
 static cudaError_t launch_fused(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int NT = KV4_NT_FUSED, ring = kWarps * Ring<D, NT>::kBytes;
+  constexpr int ring = kWarps * Ring<D>::kBytes;
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  const int rows = a.B * a.Hkv, tasks = (a.K + 1) * Ring<D, NT>::kParts;
-  const int cs = max(1, min(min(kMaxCluster, (tasks + kWarps - 1) / kWarps), sms * 3 / rows));
-  return launch_ctas(kv4_decode_fused_kernel<D, NT, CAP>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  const int rows = a.B * a.Hkv;
+  const int cs = max(1, min(min(kMaxCluster, (a.K + kWarps) / kWarps), sms * 3 / rows));
+  return launch_ctas(kv4_decode_fused_kernel<D, CAP>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
 }
 
 cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl,
@@ -1025,9 +1033,10 @@ cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Ca
   a.lse_s_out = lse_s;
   a.o = o;
   a.lse_o = lse_o;
-  const bool small = sh.NB <= 16 * 32;
-  return sh.d == 128 ? (small ? launch_fused<128, 16>(a, st) : launch_fused<128, 64>(a, st))
-                     : (small ? launch_fused<64, 16>(a, st) : launch_fused<64, 64>(a, st));
+  // blocks of a row that the selecting warp's registers hold
+  if (sh.NB <= 4 * 32) return sh.d == 128 ? launch_fused<128, 4>(a, st) : launch_fused<64, 4>(a, st);
+  if (sh.NB <= 16 * 32) return sh.d == 128 ? launch_fused<128, 16>(a, st) : launch_fused<64, 16>(a, st);
+  return sh.d == 128 ? launch_fused<128, 64>(a, st) : launch_fused<64, 64>(a, st);
 }
 
 }  // namespace sas
