@@ -131,6 +131,11 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2^x, relative error 
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {  // a NaN is passed over, as fmaxf does
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
@@ -235,9 +240,11 @@ struct Query {
   }
 };
 
-// A warp's running state. Rows of `acc` are channels: acc[j][i] holds channels
-// 32 j + 4 g + 2 i (elements 0, 1) and + 1 (elements 2, 3, times 2^4) of heads
-// 2t (even elements) and 2t + 1.
+// A warp's running state. Rows of `acc` are channels: with x and y the channels
+// 32 j + 4 g + 2 i and the one after it, acc[j][i] holds x + 16 y (elements 0,
+// 1) and 16 y (elements 2, 3) of heads 2t (even elements) and 2t + 1. A byte of
+// codes goes in whole for the first, which saves an AND, and x is taken out of
+// the two sums at the end: both have the same P·s, so its rounding cancels.
 template <int D>
 struct State {
   static constexpr int NG = D / kGroup;
@@ -312,8 +319,8 @@ __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, f
   top[1] = fmaxf(S[0][0].y, S[0][1].y);
 #pragma unroll
   for (int i = 1; i < NT; ++i) {
-    top[0] = fmaxf(top[0], fmaxf(S[i][0].x, S[i][1].x));
-    top[1] = fmaxf(top[1], fmaxf(S[i][0].y, S[i][1].y));
+    top[0] = max3(top[0], S[i][0].x, S[i][1].x);
+    top[1] = max3(top[1], S[i][0].y, S[i][1].y);
   }
 #pragma unroll
   for (int o = 4; o <= 16; o <<= 1) {
@@ -412,9 +419,9 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
       // (max(bits, lo) - lo) << 3 in both halves: the fp16 whose exponent field is the step's less lo's
       const uint32_t b0 = mul_f16x2(p0, __vmaxu2(stp[j][0], st.lo) * 8u + lo8);
       const uint32_t b1 = mul_f16x2(p1, __vmaxu2(stp[j][1], st.lo) * 8u + lo8);
-      const uint32_t a = w0.w[j], b = w1.w[j], a8 = a >> 8, b8 = b >> 8;
-      mma_f16(st.acc[j][0], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
-      mma_f16(st.acc[j][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, b0, b1);
+      const uint32_t a = w0.w[j], b = w1.w[j], a8 = __byte_perm(a, 0, 0x4341), b8 = __byte_perm(b, 0, 0x4341);
+      mma_f16(st.acc[j][0], a & 0x00ff00ffu, a & 0x00f000f0u, b & 0x00ff00ffu, b & 0x00f000f0u, b0, b1);
+      mma_f16(st.acc[j][1], a8, a8 & 0x00f000f0u, b8, b8 & 0x00f000f0u, b0, b1);
       const float x0 = bf16_of(m0, j), x1 = bf16_of(m1, j);
       st.accm[j].x = fmaf(p[i][1].x, x1, fmaf(p[i][0].x, x0, st.accm[j].x));
       st.accm[j].y = fmaf(p[i][1].y, x1, fmaf(p[i][0].y, x0, st.accm[j].y));
@@ -578,8 +585,9 @@ struct Merge {
         const int from_g = NG == 4 ? 2 * j + h : 2 * (2 * j + h);
         const float m = __shfl_sync(0xffffffffu, am[0], from_g * 4 + t) * inv;
         if (2 * t + h < G)
-          dst[(h * NG + j) * GS] = make_float4(fmaf(st.acc[j][0][h], f0, m), fmaf(st.acc[j][0][2 + h], f1, m),
-                                               fmaf(st.acc[j][1][h], f0, m), fmaf(st.acc[j][1][2 + h], f1, m));
+          dst[(h * NG + j) * GS] =
+              make_float4(fmaf(st.acc[j][0][h] - st.acc[j][0][2 + h], f0, m), fmaf(st.acc[j][0][2 + h], f1, m),
+                          fmaf(st.acc[j][1][h] - st.acc[j][1][2 + h], f0, m), fmaf(st.acc[j][1][2 + h], f1, m));
       }
     }
     if (g < CS) {
