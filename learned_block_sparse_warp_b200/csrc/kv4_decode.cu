@@ -658,7 +658,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 // The score that has an orderable key.
 __device__ __forceinline__ float key_score(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+  return __uint_as_float(k ^ (uint32_t(int(~k) >> 31) | 0x80000000u));
 }
 
 // One warp's Top-K of a score row, without a block-wide barrier: lane i holds
@@ -720,15 +720,20 @@ struct Row {
         }
         // three keys in (lo, hi), in ascending order (equal ones do no harm)
         uint32_t mid[3];
-        const float vl = key_score(lo - 1u), vh = key_score(hi - 1u);
+        if (round < 8) {
+          const float vl = key_score(lo - 1u), vh = key_score(hi - 1u);
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const uint32_t even = lo + 1u + uint32_t((uint64_t(hi - lo - 1u) * (u + 1)) >> 2);
-          const uint32_t v = score_key(fmaf(vh, 0.25f * (u + 1), vl * (0.75f - 0.25f * u))) + 1u;
-          mid[u] = round < 8 && v > lo && v < hi ? v : min(even, hi - 1u);
+          for (int u = 0; u < 3; ++u) {
+            const uint32_t v = __float_as_uint(fmaf(vh, 0.25f * (u + 1), vl * (0.75f - 0.25f * u)));
+            mid[u] = max(min((v ^ (uint32_t(int(v) >> 31) | 0x80000000u)) + 1u, hi - 1u), lo + 1u);
+          }
+          mid[1] = max(mid[1], mid[0]);
+          mid[2] = max(mid[2], mid[1]);
+        } else {
+          const uint32_t quarter = (hi - lo) / 4u;
+#pragma unroll
+          for (int u = 0; u < 3; ++u) mid[u] = min(lo + max(quarter * (u + 1), 1u), hi - 1u);
         }
-        mid[1] = max(mid[1], mid[0]);
-        mid[2] = max(mid[2], mid[1]);
         int cnt[3] = {0, 0, 0};
 #pragma unroll
         for (int i = 0; i < CAP; ++i)
