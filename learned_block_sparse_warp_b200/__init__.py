@@ -668,6 +668,7 @@ class DecodeGraph:
     between them. The three kernels are chained by programmatic dependent
     launch, so each one's launch overlaps the tail of the one before. With
     ``fused=True`` a replay is the single launch of sas_decode_fused.
+    ``DecodeGraph.kv4`` captures the steps over a 4-bit cache.
     """
 
     def __init__(self, p: Params, q, kc, vc, cache_len, s, n_split: int, out: dict, stream=None, kmean=None,
@@ -680,6 +681,25 @@ class DecodeGraph:
             self.step, self.args = decode_step, (p, q, kc, vc, cache_len, s, n_split, out)
         else:
             self.step, self.args = decode_step_scored, (p, q, kc, vc, kmean, cache_len, s, n_split, out)
+        self._capture(stream)
+
+    @classmethod
+    def kv4(cls, p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, stream=None, kmean=None,
+            k_new=None, v_new=None, fused: bool = False) -> "DecodeGraph":
+        """The same over a 4-bit cache: ``decode_step_kv4``, ``decode_step_fused_kv4`` (fused), or with kmean, k_new and
+        v_new ``decode_step_scored_kv4``. The capture runs the step once: a scored step writes its token then."""
+        self = cls.__new__(cls)
+        if kmean is not None:
+            self.step = decode_step_scored_kv4
+            self.args = (p, q, k_new, v_new, cache, kmean, cache_len, s, n_split, out)
+        elif fused:
+            self.step, self.args = decode_step_fused_kv4, (p, q, cache, cache_len, s, out)
+        else:
+            self.step, self.args = decode_step_kv4, (p, q, cache, cache_len, s, n_split, out)
+        self._capture(stream)
+        return self
+
+    def _capture(self, stream) -> None:
         side = torch.cuda.Stream() if stream is None else stream
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):  # first call outside capture: kernel attributes get set here

@@ -41,7 +41,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;      // portable cluster size
 constexpr int kMaxPicks = 255;      // one-launch form: picks of a row
 constexpr int kWarpBlocks = 64;     // blocks of a warp: a row's 256 over the 4 warps of one CTA
-constexpr float kPShift = 8.f;      // P is kept times 2^8
+constexpr float kPShift = -20.f;    // P is kept times 2^-20: sums of a million tokens of P·V stay in fp32's range
+constexpr float kPToHalf = 268435456.f;  // and goes to the tensor cores times 2^8: 2^28
 constexpr int kStepField = 17;      // exponent field that the largest step gets in fp16 when the base is set
 constexpr int kStepLimit = 23;      // a step with this field (2^8) moves the base: P·s stays under 2^16
 
@@ -65,17 +66,13 @@ struct Kv4DecodeArgs {
 
 __device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%10,%10,%10};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -99,31 +96,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t y;
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
   return y;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
-      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
-      "add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
-      "mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // -126 <= e <= 127
 __device__ __forceinline__ float exp2_approx(float x) {  // 2^x, relative error about 2^-22, 0 below 2^-126
@@ -234,7 +206,9 @@ struct Query {
     sum[1] = NG == 4 ? pack_bf16x2(part[NG - 2], part[NG - 1]) : 0u;
     const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
     const float c = scale * kLog2e * 512.f;  // 2^24 / 2^15
-    f = make_float2(c * exp2_int(min(e0, 100)), c * exp2_int(min(e1, 100)));
+    // kept positive and finite for any softmax scale: masked logits are -inf · f
+    f = make_float2(fminf(fmaxf(c * exp2_int(min(e0, 100)), 1.17549435e-38f), 3.402823466e38f),
+                    fminf(fmaxf(c * exp2_int(min(e1, 100)), 1.17549435e-38f), 3.402823466e38f));
     over = make_float2(exp2_int(max(e0 - 100, 0)), exp2_int(max(e1 - 100, 0)));
     big = __any_sync(0xffffffffu, e > 100);
   }
@@ -250,7 +224,7 @@ struct State {
   static constexpr int NG = D / kGroup;
   float acc[NG][2][4];
   float2 accm[NG];    // Σ p m over this lane's tokens, heads 2t and 2t + 1
-  float m[2], l[2];   // maximum (log2), and Σ p 2^8 over this lane's tokens
+  float m[2], l[2];   // maximum (log2), and Σ p over this lane's tokens (p times 2^-20 throughout)
   uint32_t lo;        // base of the steps' exponent field, as bf16 bits in both halves
   uint32_t lim;       // largest step bits below the limit, in both halves
 
@@ -310,7 +284,7 @@ __device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& 
   }
 }
 
-// The online softmax: S becomes p · 2^8 with p = 2^(S f + lam - max), and the
+// The online softmax: S becomes p · 2^-20 with p = 2^(S f + lam - max), and the
 // state is rescaled. (f > 0, so the largest logit is that of the largest S.)
 template <int D, int NT>
 __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[NT][2]) {
@@ -412,7 +386,8 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
       st.lo = uint32_t(now << 7) * 0x10001u;
       st.lim = uint32_t(((now + kStepLimit) << 7) - 1) * 0x10001u;
     }
-    const uint32_t p0 = transpose8x8(pack_f16x2(p[i][0].x, p[i][0].y)), p1 = transpose8x8(pack_f16x2(p[i][1].x, p[i][1].y));
+    const float2 h0 = mul_f32x2(p[i][0], make_float2(kPToHalf, kPToHalf)), h1 = mul_f32x2(p[i][1], make_float2(kPToHalf, kPToHalf));
+    const uint32_t p0 = transpose8x8(pack_f16x2(h0.x, h0.y)), p1 = transpose8x8(pack_f16x2(h1.x, h1.y));
     const uint32_t lo8 = 0u - 8u * st.lo;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
@@ -429,11 +404,10 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
   }
 }
 
-// A warp's ring: the K record of a block in one slot, its V record in the other.
-// Item 2 i is block i's K, item 2 i + 1 its V; a slot is refilled as soon as it
-// has been used. Records are named by their number (-1: a block left out).
+// A warp's copy of END bytes, 512 per instruction, the offsets as immediates
+// (address arithmetic per copy took a tenth of the loop's instructions).
 template <int O, int END>
-__device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {  // END bytes from O on, 512 per step
+__device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {
   if constexpr (O + 512 <= END) {
     asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;\n" ::"r"(dst), "l"(src), "n"(O));
     copy_lines<O + 512, END>(dst, src);
@@ -443,6 +417,9 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {  
   }
 }
 
+// A warp's ring: the K record of a block in one slot, its V record in the other.
+// Item 2 i is block i's K, item 2 i + 1 its V; a slot is refilled as soon as it
+// has been used. Records are named by their number (-1: a block left out).
 template <int D>
 struct Ring {
   static constexpr int kRecord = Fmt<D>::kRecord;
@@ -561,14 +538,14 @@ struct Merge {
       }
     }
     if (NG == 2) am[0] += __shfl_xor_sync(0xffffffffu, am[0], 4);
+    // 2^24 of the codes, 2^-28 of P, 2^-112 of the two exponents' biases
     const int lo_e = int((st.lo & 0xffffu) >> 7);
-    float f = exp2_int(min(lo_e - 88, 127));  // 2^24 of the codes, 2^-112 of the two exponents' biases
-    if (lo_e > 215) {
-      f = exp2_int(lo_e - 112);
+    const float f = exp2_int(min(lo_e, 200) - 116);
+    if (lo_e > 200) {
 #pragma unroll
       for (int j = 0; j < NG; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.acc[j][0][e] *= 16777216.f, st.acc[j][1][e] *= 16777216.f;
+        for (int e = 0; e < 4; ++e) st.acc[j][0][e] *= exp2_int(lo_e - 200), st.acc[j][1][e] *= exp2_int(lo_e - 200);
     }
     const int slot = g / CS, owner = g - slot * CS;
     float4* dst = o + from * U + 2 * t * NG * GS + slot;

@@ -320,11 +320,12 @@ def _outputs(p, n_split=None):
     return sas.empty_decode_outputs(p, n_split or 1)
 
 
-def _check(out, ref, tol_o, tol_l):
+def _check(out, ref, tol_o, tol_l, lse_s=True):
     assert_idx_equal(out["idx"].cpu().numpy(), ref["idx"])
-    lse_s = host(out["lse_s"])
-    fin = np.isfinite(ref["lse_s"])
-    assert np.array_equal(np.isfinite(lse_s), fin) and np.all(np.abs(lse_s[fin] - ref["lse_s"][fin]) < 1e-4)
+    if lse_s:
+        got = host(out["lse_s"])
+        fin = np.isfinite(ref["lse_s"])
+        assert np.array_equal(np.isfinite(got), fin) and np.all(np.abs(got[fin] - ref["lse_s"][fin]) < 1e-4)
     o, lse = host(out["o"]), host(out["lse_o"])
     worst = np.abs(lse - ref["lse"]) / tol_l
     assert np.all(worst <= 1), f"lse_o: {worst.max():.3g} of its bound"
@@ -702,3 +703,183 @@ def test_optional_outputs_and_refusals_of_the_binding():
         sas.Kv4Cache(p, st.dev["k"], st.dev["v"][:, :, :, :-1])
     with pytest.raises(sas.SasError):
         sas.sas_kv4_write(p, st.cache, k.expand(1, 2, 300, 128).contiguous(), k.expand(1, 2, 300, 128).contiguous(), cl)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# what could go wrong
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_windows_at_every_offset(d):
+    """Windows that begin and end at each of a tile's 16 tokens, in the middle of a block and across two."""
+    sas = _sas()
+    p = _params(16, 2, 2, d, 192)
+    for T in (1, 15, 16, 35, 80):
+        st = Store(p, True, seed=T)
+        k, v = _kv(16, 2, T, d, seed=T)
+        lens = [T + 23 + off for off in range(16)]
+        sas.sas_kv4_write(p, st.cache, bf16_dev(k), bf16_dev(v), _i32(lens))
+        _ok()
+        st.write(k, v, lens, [T] * 16)
+        st.same()
+
+
+def _score_rows(kind, shape, g):
+    s = (g.standard_normal(shape) * np.sqrt(2)).astype(np.float32)
+    if kind == "same":
+        s[:] = 0.75
+    elif kind == "few":
+        s = g.choice(np.array([-1.0, -0.0, 0.0, 2.0], np.float32), shape)
+    elif kind == "special":
+        s = g.choice(np.array([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-40, 3.4e38, -3.4e38, 1.0], np.float32), shape)
+    elif kind == "close":  # neighbours in fp32
+        s = (1.0 + g.integers(0, 40, shape) * 2.0 ** -23).astype(np.float32)
+    elif kind == "outlier":
+        s[..., 0], s[..., -1] = 3e38, -3e38
+    elif kind == "magnitudes":
+        s = (s * np.exp2(g.integers(-120, 120, shape))).astype(np.float32)
+    return s
+
+
+@pytest.mark.parametrize("kind", ["normal", "same", "few", "special", "close", "outlier", "magnitudes"])
+@pytest.mark.parametrize("NB", [1, 2, 5, 33, 128, 129, 512, 513, 2048])
+def test_one_launch_selection_is_the_select_kernels(NB, kind):
+    sas = _sas()
+    g = np.random.default_rng(NB)
+    s = _score_rows(kind, (3, 2, NB), g)
+    lens = [64 * NB, 64 * max(NB - 1, 1), int(g.integers(1, 64 * NB + 1))]
+    cl, sd = _i32(lens), f32_dev(s)
+    for K in sorted({1, 3, 32, 64, 255, min(NB, 255)}):
+        p = _params(3, 2, 2, 64, 64 * NB, K)
+        cache = sas.empty_kv4_cache(p)
+        cache.k.zero_(), cache.v.zero_()
+        q = torch.ones((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+        out = _outputs(p)
+        sas.decode_step_fused_kv4(p, q, cache, cl, sd, out)
+        idx, lse = torch.empty_like(out["idx"]), torch.empty_like(out["lse_s"])
+        sas.sas_topk_select(p, sd, idx, lse, cache_len=cl)
+        _ok()
+        assert torch.equal(out["idx"], idx), (NB, K, kind)
+        a, b = host(out["lse_s"]), host(lse)
+        same = (a == b) | (np.isnan(a) & np.isnan(b))
+        # a sum of up to 2048 fp32 terms in another order, each side off by log2(2048) + 16 roundings at most
+        with np.errstate(invalid="ignore"):
+            near = np.abs(a - b) <= 64 * 2.0 ** -24 * (1 + np.abs(b))
+        assert np.all(same | near), (NB, K, kind)
+        assert torch.all(out["o"] == 0)
+
+
+@pytest.mark.parametrize("gate", [O.GATE_LOG_SIGMOID, O.GATE_LOGIT])
+@pytest.mark.parametrize("form", ["fused", "split"])
+def test_gates_that_close_leave_the_current_block(gate, form):
+    """Every pick's gate is 0 (log g = -inf): rows of whole splits are empty, and the current block stands alone."""
+    p = _params(2, 8, 2, 128, 1024, 9, gate)
+    lens = [1024, 700]
+    st = _filled(p, True, seed=3, lens=lens)
+    q, s = _qs(p, seed=3)
+    s[0] = -np.inf
+    s[1, :, ::2] = -np.inf
+    out = _run(p, st, q, lens, s, 5, form)
+    # the same picks and the same outputs as of gates of e^-200, which are below every rounding here
+    _check(out, *_reference(p, st, q, lens, np.where(np.isfinite(s), s, np.float32(-200.0))), lse_s=False)
+    if form == "split":
+        lp = host(out["lse_part"])
+        assert np.all(lp[0, :, 1:] == -np.inf) and torch.all(out["o_part"][0, :, 1:] == 0)
+
+
+@pytest.mark.parametrize("form", ["fused", "split"])
+@pytest.mark.parametrize("qs,ks,vs", [(1e33, 1e-33, 1.0), (1e-30, 1e30, 1.0), (1.0, 1.0, 1e37), (1.0, 1.0, 1e-36)])
+def test_decode_at_the_ends_of_the_range(qs, ks, vs, form):
+    p = _params(2, 8, 2, 128, 512, 3)
+    lens = [512, 77]
+    st = Store(p, False, seed=5, fill=0xFF)
+    k, _ = _kv(2, 2, 512, 128, seed=5, scale=ks)
+    _, v = _kv(2, 2, 512, 128, seed=6, scale=vs)
+    st.write(k, v, lens, lens)
+    st.handle()
+    q, s = _qs(p, seed=7, scale=qs)
+    _check(_run(p, st, q, lens, s, 2, form), *_reference(p, st, q, lens, s))
+
+
+def test_merge_has_the_same_bits_for_few_and_many_rows():
+    """sas_decode_combine spreads few rows over more warps; a row's result does not depend on that, nor on NaN next to it."""
+    sas = _sas()
+    for d in (64, 128):
+        for n in (1, 9, 33, 64):
+            g = torch.Generator(device="cuda").manual_seed(n)
+            few, many = _params(8, 32, 8, d, 4096, 64), _params(9, 32, 8, d, 4096, 64)  # 256 and 288 rows
+            o_part = torch.randn((9, 32, n, d), device="cuda", generator=g)
+            lse_part = 3 * torch.randn((9, 32, n), device="cuda", generator=g)
+            lse_part[1, 3, 0] = -np.inf
+            lse_part[2, 5] = -np.inf
+            lse_part[4, 6, n - 1] = np.nan
+            o_part[4, 6, n - 1] = np.nan
+            res = []
+            for p in (few, many):
+                o = torch.empty((p.batch, 32, d), dtype=torch.bfloat16, device="cuda")
+                lse = torch.empty((p.batch, 32), dtype=torch.float32, device="cuda")
+                sas.sas_decode_combine(p, n, o_part[:p.batch].contiguous(), lse_part[:p.batch].contiguous(), o, lse)
+                res.append((o, lse))
+            _ok()
+            assert torch.equal(res[0][0].view(torch.int16), res[1][0][:8].view(torch.int16))
+            a, b = res[0][1], res[1][1][:8]
+            assert torch.equal(torch.nan_to_num(a, nan=7.0), torch.nan_to_num(b, nan=7.0))
+            assert torch.isnan(res[0][0][4, 6]).all() and torch.isnan(a[4, 6]) and torch.isnan(a).sum() == 1
+            assert torch.all(res[0][0][2, 5] == 0) and a[2, 5] == -np.inf
+
+
+def test_two_streams_at_once():
+    """Steps of two batches on two streams, none waiting for the other, give what each gives alone."""
+    sas = _sas()
+    runs = []
+    for seed, (d, Lmax, K) in ((1, (128, 2048, 8)), (2, (64, 1024, 5))):
+        p = _params(3, 12, 3, d, Lmax, K, O.GATE_LOG_SOFTMAX)
+        lens = [Lmax, Lmax // 2 + 5, 70]
+        st = _filled(p, True, seed=seed, lens=lens)
+        q, s = _qs(p, seed=seed)
+        alone = (_run(p, st, q, lens, s, 2, "fused"), _run(p, st, q, lens, s, 2, "split"))
+        runs.append((p, st, bf16_dev(q), _i32(lens), f32_dev(s), alone, [_outputs(p, 2) for _ in range(2)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, st, q, cl, s, alone, outs, stream in runs:
+            sas.decode_step_fused_kv4(p, q, st.cache, cl, s, outs[0], stream=stream)
+            sas.decode_step_kv4(p, q, st.cache, cl, s, 2, outs[1], stream=stream)
+    _ok()
+    for p, st, q, cl, s, alone, outs, stream in runs:
+        for want, got in zip(alone, outs):
+            assert all(torch.equal(want[k], got[k]) for k in ("o", "lse_o", "idx", "lse_s"))
+
+
+def test_captured_steps():
+    """DecodeGraph.kv4: the three steps, replayed on new inputs, are the eager ones."""
+    sas = _sas()
+    p = _params(2, 8, 2, 128, 512, 3)
+    lens = [300, 64]
+    st = _filled(p, True, seed=2, lens=lens)
+    q, s = _qs(p, seed=5)
+    qd, sd, cl = bf16_dev(q), f32_dev(s), _i32(lens)
+    km = torch.zeros((2, 2, 8, 128), dtype=torch.bfloat16, device="cuda")
+    sas.sas_kv4_block_mean_keys(p, st.cache, 300, cl, km, cl)
+    k, v = _kv(2, 2, 3, 128, seed=6)
+    kd, vd = bf16_dev(k[:, :, :1]), bf16_dev(v[:, :, :1])
+    outs = [_outputs(p, 2) for _ in range(3)]
+    s3 = torch.zeros_like(sd)
+    graphs = [sas.DecodeGraph.kv4(p, qd, st.cache, cl, sd, 2, outs[0], fused=True),
+              sas.DecodeGraph.kv4(p, qd, st.cache, cl, sd, 2, outs[1]),
+              sas.DecodeGraph.kv4(p, qd, st.cache, cl, s3, 2, outs[2], kmean=km, k_new=kd, v_new=vd)]
+    for i in range(3):
+        q, s = _qs(p, seed=30 + i)
+        cl.copy_(_i32([L + i for L in lens]))
+        for dst, src in ((qd, q), (kd, k[:, :, i:i + 1]), (vd, v[:, :, i:i + 1])):
+            dst.copy_(bf16_dev(src))
+        sd.copy_(f32_dev(s))
+        for g in reversed(graphs):  # the scored one first: it writes the token that all of them read
+            g.replay()
+        want = [_outputs(p, 2) for _ in range(3)]
+        sas.decode_step_fused_kv4(p, qd, st.cache, cl, sd, want[0])
+        sas.decode_step_kv4(p, qd, st.cache, cl, sd, 2, want[1])
+        sas.decode_step_scored_kv4(p, qd, kd, vd, st.cache, km, cl, torch.zeros_like(s3), 2, want[2])
+        _ok()
+        for a, b in zip(want, outs):
+            assert all(torch.equal(a[x], b[x]) for x in ("o", "lse_o", "idx", "lse_s"))
+    with pytest.raises(ValueError):
+        sas.decode_step_scored_kv4(p, qd, bf16_dev(k), bf16_dev(v), st.cache, km, cl, s3, 2, outs[2])
