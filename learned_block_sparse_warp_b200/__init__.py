@@ -146,6 +146,10 @@ class Params:
     softmax_scale: float = 0.0
     gate_mode: int = SAS_GATE_LOG_SOFTMAX
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_shapes", None)
+        object.__setattr__(self, name, value)
+
     @property
     def n_blocks(self) -> int:
         return self.seq_len // self.block
@@ -387,17 +391,45 @@ def kv4_record_bytes(head_dim: int) -> int:
     return 40 * head_dim
 
 
+class _Kv4Shapes:
+    """The C struct and the tensor shapes of a Params, made once (a Params that changes makes them anew): a call's
+    host time is a few microseconds, and building these was one of them."""
+
+    __slots__ = ("c", "cache", "lens", "q", "s", "idx", "lse_s", "lse_o", "kmean")
+
+    def __init__(self, p: Params):
+        B, Hq, Hkv, d, NB = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim, p.n_blocks
+        self.c, self.cache, self.lens = p.c(), (B, Hkv, d, p.seq_len), (B,)
+        self.q, self.s, self.idx = (B, Hq, d), (B, Hkv, NB), (B, Hkv, p.top_k)
+        self.lse_s, self.lse_o, self.kmean = (B, Hkv), (B, Hq), (B, Hkv, NB, d)
+
+    @staticmethod
+    def of(p: Params) -> "_Kv4Shapes":
+        sh = p.__dict__.get("_shapes")
+        if sh is None:
+            sh = p.__dict__["_shapes"] = _Kv4Shapes(p)
+        return sh
+
+
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _arg(t, dtype, shape, name: str, dev: int):
     """Pointer of a tensor of the call, checked; dev is the current device, which the launch goes to."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: expected a CUDA tensor on the current device cuda:{dev}, got {t.device}")
-        _ptr(t, dtype, shape, name)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a CUDA tensor on the current device cuda:{dev}, got {t.device}")
+    return _ptr(t, dtype, shape, name)
 
 
 def _opt(t, dtype, shape, name: str, dev: int):
     return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _stream_on(dev: int, stream):
+    """The stream's handle; the current stream of device dev when it is None."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 class Kv4Cache:
@@ -424,14 +456,13 @@ class Kv4Cache:
         self._ref = ctypes.byref(self._c)
 
     def of(self, p: Params):
-        """The C struct, once p has been checked against the cache's shape and the current device."""
-        if self.dims != (p.batch, p.n_kv_heads, p.head_dim, p.seq_len):
-            raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self.dims}, called with "
-                             f"{(p.batch, p.n_kv_heads, p.head_dim, p.seq_len)}")
-        if self.device != torch.cuda.current_device():
-            raise ValueError(f"cache: lies on cuda:{self.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        return self._ref
+        """(C struct, shapes of p), once p has been checked against the cache's shape and the current device."""
+        sh = _Kv4Shapes.of(p)
+        if self.dims != sh.cache:
+            raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self.dims}, called with {sh.cache}")
+        if self.device != _device():
+            raise ValueError(f"cache: lies on cuda:{self.device}, the current device is cuda:{_device()}")
+        return self._ref, sh
 
 
 def empty_kv4_cache(p: Params, n_pages: Optional[int] = None, block_table: Optional[torch.Tensor] = None,
@@ -454,59 +485,60 @@ def _tokens(t, name: str) -> int:
 
 def sas_kv4_write(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
     """Quantises k, v [B, Hkv, T, d] into the cache at positions cache_len - new_len .. cache_len - 1 (new_len: T)."""
-    c, dev, T = cache.of(p), cache.device, _tokens(k, "k")
-    sh = (p.batch, p.n_kv_heads, T, p.head_dim)
+    ref, sh = cache.of(p)
+    dev, T = cache.device, _tokens(k, "k")
+    kv = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_write", lib.sas_kv4_write(
-        p.c(), c, T, _arg(k, bf16, sh, "k", dev), _arg(v, bf16, sh, "v", dev),
-        _arg(cache_len, i32, (p.batch,), "cache_len", dev), _opt(new_len, i32, (p.batch,), "new_len", dev),
-        _stream(stream)))
+        sh.c, ref, T, _arg(k, bf16, kv, "k", dev), _arg(v, bf16, kv, "v", dev),
+        _arg(cache_len, i32, sh.lens, "cache_len", dev), _opt(new_len, i32, sh.lens, "new_len", dev),
+        _stream_on(dev, stream)))
 
 
 def sas_kv4_read(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
     """Reads back what ``sas_kv4_write`` wrote under the same lengths into k, v [B, Hkv, T, d] (either may be None)."""
-    c, dev = cache.of(p), cache.device
+    ref, sh = cache.of(p)
     if k is None and v is None:
         raise ValueError("k, v: at least one output is needed")
-    T = _tokens(v, "v") if k is None else _tokens(k, "k")
-    sh = (p.batch, p.n_kv_heads, T, p.head_dim)
+    dev, T = cache.device, _tokens(v, "v") if k is None else _tokens(k, "k")
+    kv = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_read", lib.sas_kv4_read(
-        p.c(), c, T, _opt(k, bf16, sh, "k", dev), _opt(v, bf16, sh, "v", dev),
-        _arg(cache_len, i32, (p.batch,), "cache_len", dev), _opt(new_len, i32, (p.batch,), "new_len", dev),
-        _stream(stream)))
+        sh.c, ref, T, _opt(k, bf16, kv, "k", dev), _opt(v, bf16, kv, "v", dev),
+        _arg(cache_len, i32, sh.lens, "cache_len", dev), _opt(new_len, i32, sh.lens, "new_len", dev),
+        _stream_on(dev, stream)))
 
 
 def sas_kv4_block_mean_keys(p: Params, cache: Kv4Cache, n_tokens: int, cache_len, kmean, new_len=None,
                             stream=None) -> None:
     """Block means of the blocks that the last new_len (default n_tokens) tokens completed, into kmean [B, Hkv, NKB, d]."""
-    c, dev = cache.of(p), cache.device
+    ref, sh = cache.of(p)
+    dev = cache.device
     _check("sas_kv4_block_mean_keys", lib.sas_kv4_block_mean_keys(
-        p.c(), c, n_tokens, _arg(cache_len, i32, (p.batch,), "cache_len", dev),
-        _opt(new_len, i32, (p.batch,), "new_len", dev),
-        _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", dev), _stream(stream)))
+        sh.c, ref, n_tokens, _arg(cache_len, i32, sh.lens, "cache_len", dev),
+        _opt(new_len, i32, sh.lens, "new_len", dev), _arg(kmean, bf16, sh.kmean, "kmean", dev), _stream_on(dev, stream)))
 
 
 def sas_decode_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, idx, lse_s, n_split: int, o_part, lse_part,
                    stream=None) -> None:
     """sas_decode over a 4-bit cache."""
-    c, dev = cache.of(p), cache.device
-    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+    ref, sh = cache.of(p)
+    dev = cache.device
+    B, Hq, d = sh.q
     _check("sas_decode_kv4", lib.sas_decode_kv4(
-        p.c(), _arg(q, bf16, (B, Hq, d), "q", dev), c, _arg(cache_len, i32, (B,), "cache_len", dev),
-        _opt(s, f32, (B, Hkv, p.n_blocks), "s", dev), _arg(idx, i32, (B, Hkv, p.top_k), "idx", dev),
-        _opt(lse_s, f32, (B, Hkv), "lse_s", dev), n_split, _arg(o_part, f32, (B, Hq, n_split, d), "o_part", dev),
-        _arg(lse_part, f32, (B, Hq, n_split), "lse_part", dev), _stream(stream)))
+        sh.c, _arg(q, bf16, sh.q, "q", dev), ref, _arg(cache_len, i32, sh.lens, "cache_len", dev),
+        _opt(s, f32, sh.s, "s", dev), _arg(idx, i32, sh.idx, "idx", dev), _opt(lse_s, f32, sh.lse_s, "lse_s", dev),
+        n_split, _arg(o_part, f32, (B, Hq, n_split, d), "o_part", dev),
+        _arg(lse_part, f32, (B, Hq, n_split), "lse_part", dev), _stream_on(dev, stream)))
 
 
 def sas_decode_fused_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, o, idx=None, lse_s=None, lse_o=None,
                          stream=None) -> None:
     """sas_decode_fused over a 4-bit cache: select, attention and merge in one launch."""
-    c, dev = cache.of(p), cache.device
-    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+    ref, sh = cache.of(p)
+    dev = cache.device
     _check("sas_decode_fused_kv4", lib.sas_decode_fused_kv4(
-        p.c(), _arg(q, bf16, (B, Hq, d), "q", dev), c, _arg(cache_len, i32, (B,), "cache_len", dev),
-        _arg(s, f32, (B, Hkv, p.n_blocks), "s", dev), _opt(idx, i32, (B, Hkv, p.top_k), "idx", dev),
-        _opt(lse_s, f32, (B, Hkv), "lse_s", dev), _arg(o, bf16, (B, Hq, d), "o", dev),
-        _opt(lse_o, f32, (B, Hq), "lse_o", dev), _stream(stream)))
+        sh.c, _arg(q, bf16, sh.q, "q", dev), ref, _arg(cache_len, i32, sh.lens, "cache_len", dev),
+        _arg(s, f32, sh.s, "s", dev), _opt(idx, i32, sh.idx, "idx", dev), _opt(lse_s, f32, sh.lse_s, "lse_s", dev),
+        _arg(o, bf16, sh.q, "o", dev), _opt(lse_o, f32, sh.lse_o, "lse_o", dev), _stream_on(dev, stream)))
 
 
 def sas_selftest_wait_timeout(stream=None) -> None:
@@ -612,16 +644,16 @@ def decode_step_scored(p: Params, q, kc, vc, kmean, cache_len, s, n_split: int, 
 def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream) -> None:
     """Select, split-K attention and merge over a 4-bit cache, every argument checked once and before the first
     launch. select(c, pointers..., stream) launches the selection."""
-    ref, dev, st = cache.of(p), cache.device, _stream(stream)
-    B, Hq, Hkv, d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
-    qp, lp = _arg(q, bf16, (B, Hq, d), "q", dev), _arg(cache_len, i32, (B,), "cache_len", dev)
-    sp = _arg(s, f32, (B, Hkv, p.n_blocks), "s", dev)
-    ip = _arg(out["idx"], i32, (B, Hkv, p.top_k), "idx", dev)
-    ep = _arg(out["lse_s"], f32, (B, Hkv), "lse_s", dev)
+    ref, sh = cache.of(p)
+    dev, c, st = cache.device, sh.c, _stream_on(cache.device, stream)
+    B, Hq, d = sh.q
+    qp, lp = _arg(q, bf16, sh.q, "q", dev), _arg(cache_len, i32, sh.lens, "cache_len", dev)
+    sp = _arg(s, f32, sh.s, "s", dev)
+    ip = _arg(out["idx"], i32, sh.idx, "idx", dev)
+    ep = _arg(out["lse_s"], f32, sh.lse_s, "lse_s", dev)
     op = _arg(out["o_part"], f32, (B, Hq, n_split, d), "o_part", dev)
     xp = _arg(out["lse_part"], f32, (B, Hq, n_split), "lse_part", dev)
-    yp, zp = _arg(out["o"], bf16, (B, Hq, d), "o", dev), _opt(out.get("lse_o"), f32, (B, Hq), "lse_o", dev)
-    c = p.c()
+    yp, zp = _arg(out["o"], bf16, sh.q, "o", dev), _opt(out.get("lse_o"), f32, sh.lse_o, "lse_o", dev)
     select(c, qp, lp, sp, ip, ep, st)
     _check("sas_decode_kv4", lib.sas_decode_kv4(c, qp, ref, lp, sp, ip, ep, n_split, op, xp, st))
     _check("sas_decode_combine", lib.sas_decode_combine(c, n_split, op, xp, yp, zp, st))
