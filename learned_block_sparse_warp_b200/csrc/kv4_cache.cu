@@ -195,19 +195,19 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 28 / kWriteWarps) kv4_write_
   const int j = lane % LPR >> 1, hq = lane & 1, at = lane / LPR;
   const uint16_t* src = (is_v ? v : k) + (int64_t(t.b * a.Hkv + t.h) * a.n_tokens + t.i0) * D + 32 * j + 8 * hq;
   uint4 x[NI][2];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = i * TPI + at;
-    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-    if (r >= t.r0 && r < t.r1) {
-      x[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D));
-      x[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D + 16));
-    }
-  }
-  const int rec = record_of(a.c, t.b, t.h, t.m, a.Hkv, a.Lmax / kBlock, a.err);
-  if (rec < 0) return;
-  uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + t.in_block * F::kTileBytes;
   if (t.r1 - t.r0 < kTile) {  // a part of the tile: the other tokens' bits stay as they are
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * TPI + at;
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      if (r >= t.r0 && r < t.r1) {
+        x[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D));
+        x[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + int64_t(r) * D + 16));
+      }
+    }
+    const int rec = record_of(a.c, t.b, t.h, t.m, a.Hkv, a.Lmax / kBlock, a.err);
+    if (rec < 0) return;
+    uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + t.in_block * F::kTileBytes;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if (i * TPI + TPI <= t.r0 || i * TPI >= t.r1) continue;
@@ -217,6 +217,15 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 28 / kWriteWarps) kv4_write_
     }
     return;
   }
+  src += at * D;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    x[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + i * TPI * D));
+    x[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + i * TPI * D + 16));
+  }
+  const int rec = record_of(a.c, t.b, t.h, t.m, a.Hkv, a.Lmax / kBlock, a.err);
+  if (rec < 0) return;
+  uint8_t* tile = (is_v ? a.c.v : a.c.k) + size_t(rec) * F::kRecord + t.in_block * F::kTileBytes;
   // the whole tile: staged, so that it leaves in 16-byte stores
   uint8_t* stage = stage_s[warp];
 #pragma unroll
