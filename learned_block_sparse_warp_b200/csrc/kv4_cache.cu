@@ -380,30 +380,18 @@ __device__ __forceinline__ float2 nibble_pair(uint32_t w, int c) {
                    make_float2(-__uint_as_float(ex), -__uint_as_float(ey)));
 }
 
-// One warp per (sequence, KV head, candidate block). A lane sums the 8 tokens
-// g, g + 8, ... of its t, 8 channels per group; the lanes of a t are then added
-// pairwise, each keeping half of the channels.
+// The mean key of a K record, by a warp. A lane sums the 8 tokens g, g + 8, ...
+// of its t, 8 channels per group; the lanes of a t are then added pairwise, each
+// keeping half of the channels.
 template <int D>
-__global__ void __launch_bounds__(128) kv4_means_kernel(Kv4Args a, unsigned per, uint16_t* __restrict__ kmean) {
+__device__ __forceinline__ void mean_of(const uint8_t* rec, uint16_t* out) {
   using F = Fmt<D>;
   constexpr int NG = F::NG;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int NB = a.Lmax / kBlock;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const unsigned item = blockIdx.x * 4 + (threadIdx.x >> 5), bh = item / per;
-  if (bh >= unsigned(a.B) * a.Hkv) return;
-  const int b = int(bh / a.Hkv), h = int(bh % a.Hkv);
-  const Window wd = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
-  const int m = wd.pos / kBlock + int(item % per);
-  if (wd.n == 0 || kBlock * (m + 1) > wd.pos + wd.n) return;
-  const int rec = record_of(a.c, b, h, m, a.Hkv, NB, a.err);
-  if (rec < 0) return;
-  const uint8_t* base = a.c.k + size_t(rec) * F::kRecord;
   uint32_t w[2 * kTiles][NG], s[2 * kTiles][NG / 2], lo[2 * kTiles][NG / 2];
 #pragma unroll
   for (int i = 0; i < 2 * kTiles; ++i) {
-    const uint8_t* tile = base + i / 2 * F::kTileBytes;
+    const uint8_t* tile = rec + i / 2 * F::kTileBytes;
     const int r = g + 8 * (i & 1);
     load_words<NG>(tile + F::k_word(r, t, 0), w[i]);
     load_words<NG / 2>(tile + F::k_step(r, 0), s[i]);
@@ -440,12 +428,52 @@ __global__ void __launch_bounds__(128) kv4_means_kernel(Kv4Args a, unsigned per,
     }
   }
   // this lane has the N/8 channels from N/8 · g of its t's list
-  uint16_t* out = kmean + (size_t(bh) * NB + m) * D;
   const int c0 = g * (N / 8), ch = 32 * (c0 / 8) + 8 * t + c0 % 8;
   if (NG == 4)
     *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_bf16x2(x[0] / kBlock, x[1] / kBlock), pack_bf16x2(x[2] / kBlock, x[3] / kBlock));
   else
     *reinterpret_cast<uint32_t*>(out + ch) = pack_bf16x2(x[0] / kBlock, x[1] / kBlock);
+}
+
+// Candidate block `item` of [bh][block]: its K record, or -1 where the new
+// tokens have not completed it. row: its place among the means.
+__device__ __forceinline__ int completed(const Kv4Args& a, unsigned item, unsigned per, size_t* row) {
+  const unsigned bh = item / per;
+  if (bh >= unsigned(a.B) * a.Hkv) return -1;
+  const int b = int(bh / a.Hkv), h = int(bh % a.Hkv), NB = a.Lmax / kBlock;
+  const Window wd = window_of(a.cache_len, a.new_len, b, a.n_tokens, a.Lmax, a.err);
+  const int m = wd.pos / kBlock + int(item % per);
+  if (wd.n == 0 || kBlock * (m + 1) > wd.pos + wd.n) return -1;
+  *row = size_t(bh) * NB + m;
+  return record_of(a.c, b, h, m, a.Hkv, NB, a.err);
+}
+
+constexpr int kMeanWarps = 4;
+
+// One warp per candidate block. The record comes through shared memory, by ten
+// copies a lane: 32768 records of d = 128 take 41 us so, 4.1 TB/s, against 51 us
+// straight from global memory in registers and 42 us with a persistent grid and
+// a ring of two records a warp; 8192 take 11 us. What bounds it is the
+// arithmetic: 850 instructions a record, half of them on the half-rate integer
+// pipe.
+template <int D>
+__global__ void __launch_bounds__(32 * kMeanWarps, 28 / kMeanWarps) kv4_means_kernel(Kv4Args a, unsigned per, uint16_t* __restrict__ kmean) {
+  constexpr int kRecord = Fmt<D>::kRecord;
+  __shared__ __align__(16) uint8_t rec_s[kMeanWarps][kRecord];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  size_t row;
+  const int rec = completed(a, blockIdx.x * kMeanWarps + warp, per, &row);
+  if (rec < 0) return;
+  const uint8_t* src = a.c.k + size_t(rec) * kRecord + lane * 16;
+  const uint32_t dst = smem_u32(rec_s[warp]) + lane * 16;
+#pragma unroll
+  for (int o = 0; o < kRecord; o += 512) cp_async16(dst + o, src + o);
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+  mean_of<D>(rec_s[warp], kmean + row * D);
 }
 
 static Kv4Args kv4_args(const Shape& sh, const Cache& c, int n_tokens, const int32_t* cache_len,
@@ -486,8 +514,8 @@ cudaError_t launch_kv4_means(const Shape& sh, const Cache& c, int n_tokens, cons
   const Kv4Args a = kv4_args(sh, c, n_tokens, cache_len, new_len, err);
   const unsigned per = unsigned(n_tokens + kBlock - 1) / kBlock;  // the most blocks that n_tokens tokens can complete
   unsigned n;
-  if (!kv4_grid(sh, per, 4, &n)) return cudaErrorInvalidConfiguration;
-  return launch_pdl(sh.d == 128 ? kv4_means_kernel<128> : kv4_means_kernel<64>, dim3(n), dim3(128), 0, st, a, per, kmean);
+  if (!kv4_grid(sh, per, kMeanWarps, &n)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(sh.d == 128 ? kv4_means_kernel<128> : kv4_means_kernel<64>, dim3(n), dim3(32 * kMeanWarps), 0, st, a, per, kmean);
 }
 
 }  // namespace sas
