@@ -257,7 +257,8 @@ SAS_API sas_status sas_decode_paged(const sas_params* p, const sas_bf16* q, cons
 /* Merge of the split partials:
  *   LSE = log Σ_j exp lse_part[j],   o = Σ_j exp(lse_part[j] − LSE) · o_part[j].
  *   o      bf16 [B, Hq, d]. Output.
- *   lse_o  fp32 [B, Hq]. Output, may be NULL. */
+ *   lse_o  fp32 [B, Hq]. Output, may be NULL.
+ * A partial whose lse_part is NaN makes its row NaN. */
 SAS_API sas_status sas_decode_combine(const sas_params* p, int n_split, const float* o_part, const float* lse_part,
                               sas_bf16* o, float* lse_o, void* stream);
 
@@ -422,8 +423,11 @@ SAS_API sas_status sas_kv4_block_mean_keys(const sas_params* p, const sas_kv4_ca
 
 /* sas_decode over the 4-bit cache, dense or paged: the same block list, gate
  * modes, splits and outputs, merged by sas_decode_combine. The cache's values
- * s·code + m enter the products unrounded. The logits are exact to fp32, and
- * P·s is rounded to 11 bits for P·V. */
+ * s·code + m enter the products unrounded. The logits are exact to fp32; P and
+ * P·s are rounded to 11 bits for P·V. A V step under 2^-16 of the largest one
+ * of the row is not resolved there, which moves an output by less than 2^-13 of
+ * that largest step. A NaN group of K makes the row NaN, one of V its 32
+ * channels. n_pages · Hkv is at most 2^25. */
 SAS_API sas_status sas_decode_kv4(const sas_params* p, const sas_bf16* q, const sas_kv4_cache* cache,
                                   const int32_t* cache_len, const float* s, const int32_t* idx, const float* lse_s,
                                   int n_split, float* o_part, float* lse_part, void* stream);

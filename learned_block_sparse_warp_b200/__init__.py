@@ -416,6 +416,8 @@ _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 def _arg(t, dtype, shape, name: str, dev: int):
     """Pointer of a tensor of the call, checked; dev is the current device, which the launch goes to."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.get_device() != dev:
@@ -478,6 +480,8 @@ def empty_kv4_cache(p: Params, n_pages: Optional[int] = None, block_table: Optio
 
 
 def _tokens(t, name: str) -> int:
+    if t is None:
+        raise ValueError(f"{name}: missing")
     if t.dim() != 4:
         raise ValueError(f"{name}: expected [B, Hkv, T, d], got shape {tuple(t.shape)}")
     return t.shape[2]
