@@ -214,11 +214,14 @@ struct Query {
   }
 };
 
-// A warp's running state. Rows of `acc` are channels: with x and y the channels
-// 32 j + 4 g + 2 i and the one after it, acc[j][i] holds x + 16 y (elements 0,
-// 1) and 16 y (elements 2, 3) of heads 2t (even elements) and 2t + 1. A byte of
-// codes goes in whole for the first, which saves an AND, and x is taken out of
-// the two sums at the end: both have the same P·s, so its rounding cancels.
+// A warp's running state. Rows of `acc` are channels: acc[j][i] holds channel
+// 32 j + 4 g + 2 i (elements 0, 1) and 16 times the one after it (elements 2,
+// 3) of heads 2t (even elements) and 2t + 1. Each nibble is masked out for a
+// row of its own. Whole bytes (x + 16 y, with x taken out of the difference at
+// the end) save an AND of 700 instructions' 32 and 3 % of the time, but the
+// tensor cores truncate their sums, and the difference has 17 times that error:
+// over all 2048 blocks of a row, whose outputs are small next to Σ p s code, it
+// cost a bit of the output.
 template <int D>
 struct State {
   static constexpr int NG = D / kGroup;
@@ -394,9 +397,9 @@ __device__ __forceinline__ void value_block(const uint8_t* rec, State<D>& st, in
       // (max(bits, lo) - lo) << 3 in both halves: the fp16 whose exponent field is the step's less lo's
       const uint32_t b0 = mul_f16x2(p0, __vmaxu2(stp[j][0], st.lo) * 8u + lo8);
       const uint32_t b1 = mul_f16x2(p1, __vmaxu2(stp[j][1], st.lo) * 8u + lo8);
-      const uint32_t a = w0.w[j], b = w1.w[j], a8 = __byte_perm(a, 0, 0x4341), b8 = __byte_perm(b, 0, 0x4341);
-      mma_f16(st.acc[j][0], a & 0x00ff00ffu, a & 0x00f000f0u, b & 0x00ff00ffu, b & 0x00f000f0u, b0, b1);
-      mma_f16(st.acc[j][1], a8, a8 & 0x00f000f0u, b8, b8 & 0x00f000f0u, b0, b1);
+      const uint32_t a = w0.w[j], b = w1.w[j], a8 = a >> 8, b8 = b >> 8;
+      mma_f16(st.acc[j][0], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0, b1);
+      mma_f16(st.acc[j][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u, b0, b1);
       const float x0 = bf16_of(m0, j), x1 = bf16_of(m1, j);
       st.accm[j].x = fmaf(p[i][1].x, x1, fmaf(p[i][0].x, x0, st.accm[j].x));
       st.accm[j].y = fmaf(p[i][1].y, x1, fmaf(p[i][0].y, x0, st.accm[j].y));
@@ -563,8 +566,8 @@ struct Merge {
         const float m = __shfl_sync(0xffffffffu, am[0], from_g * 4 + t) * inv;
         if (2 * t + h < G)
           dst[(h * NG + j) * GS] =
-              make_float4(fmaf(st.acc[j][0][h] - st.acc[j][0][2 + h], f0, m), fmaf(st.acc[j][0][2 + h], f1, m),
-                          fmaf(st.acc[j][1][h] - st.acc[j][1][2 + h], f0, m), fmaf(st.acc[j][1][2 + h], f1, m));
+              make_float4(fmaf(st.acc[j][0][h], f0, m), fmaf(st.acc[j][0][2 + h], f1, m),
+                          fmaf(st.acc[j][1][h], f0, m), fmaf(st.acc[j][1][2 + h], f1, m));
       }
     }
     if (g < CS) {

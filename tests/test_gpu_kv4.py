@@ -475,6 +475,47 @@ def test_many_blocks_per_split_and_full_scope():
     _check(_run(p, st, q, lens, s, 40, "split"), *_reference(p, st, q, lens, s))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_that_are_small_next_to_their_terms(d):
+    """Attention over a whole cache of 65536 tokens: o is a mean of many values, 200 times smaller than sum p s code
+    and sum p |m| that it is made of, and keeps what rounding P and P*s leaves of it.
+
+    Bound of the root mean square of o's error over the channels, before any run. Two roundings to 11 bits, each off by
+    2^-11/sqrt(3) of p s code at most, in root mean square, and of one token independent of another's:
+    sqrt(2/3) 2^-11 sqrt(sum (p s code)^2). The sums of a warp's 64 tiles, each cut off by half of 2^-23 of a partial
+    sum, on average half the last one: 64 * 2^-25 sum p s code. The minima, the merges, sum p and the logits, in fp32 and
+    rounded to nearest: 2^-22 of the sums, and 2^-20 (a weight's relative error) of a term each.
+    """
+    T = 65536
+    p = _params(1, 36, 18, d, T, T // 64)  # 18 KV heads: CTAs enough without clusters, 16 blocks a warp
+    g = np.random.default_rng(d)
+    st = Store(p, False, seed=1, fill=0)
+    n = (T // 64, 64)
+    for side in "kv":
+        step = KV._bf16_bits((0.18 + 0.2 * g.random((*n, d // 32))).astype(np.float32))
+        low = KV._bf16_bits((-KV._bf16_value(step) * (7.5 + 1.5 * g.standard_normal(step.shape))).astype(np.float32))
+        st.put(side, 0, 0, KV.pack(g.integers(0, 16, (*n, d)).astype(np.uint8), step, low, side))
+    st.handle()
+    q, s = _qs(p, seed=d)
+    out = _run(p, st, q, [T], s, 17, "split")
+    codes, step, low = (x.reshape(T, -1) for x in KV._raw(st.rows("v", 0, 0), "v"))
+    term = codes * np.repeat(KV._bf16_value(step), 32, -1)
+    v = term + np.repeat(KV._bf16_value(low), 32, -1)
+    k = KV.unpack(st.rows("k", 0, 0), "k").reshape(T, d)
+    lp, op = host(out["lse_part"])[0], host(out["o_part"])[0]  # the fp32 partials: o itself is rounded to bf16
+    for h in range(2):
+        z = k @ q[0, h].astype(np.float64) / np.sqrt(d)
+        pr = np.exp(z - O.logsumexp(z))
+        w = np.exp(lp[h].astype(np.float64) - O.logsumexp(lp[h].astype(np.float64)))
+        err = (w[:, None] * op[h]).sum(0) - pr @ v
+        rms = lambda x: np.sqrt(np.mean(x ** 2))
+        sums = rms(pr @ term) + rms(pr @ (v - term))
+        squares = np.sqrt(np.mean(pr ** 2 @ term ** 2))
+        bound = np.sqrt(2 / 3) * 2.0 ** -11 * squares + (64 * 2.0 ** -25 + 2.0 ** -22) * sums + 2.0 ** -20 * squares
+        print(f"head {h}: error {rms(err):.3g}, bound {bound:.3g}, o {rms(pr @ v):.3g}")
+        assert rms(err) <= bound
+
+
 @pytest.mark.parametrize("form", ["fused", "split"])
 def test_bad_lengths_indices_and_pages_are_reported(form):
     sas = _sas()
