@@ -137,6 +137,32 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The score that has an orderable key.
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float(k ^ (uint32_t(int(~k) >> 31) | 0x80000000u));
+}
+
+// A step of a threshold search over keys + 1: three of them inside (lo, hi),
+// hi − lo >= 2, in ascending order (equal ones do no harm). They quarter the
+// range, at first that of the scores, which spread evenly over their own range,
+// and after 8 steps that of the keys, which ends for sure.
+__device__ __forceinline__ void quarter_keys(uint32_t lo, uint32_t hi, int round, uint32_t (&mid)[3]) {
+  if (round < 8) {
+    const float vl = key_score(lo - 1u), vh = key_score(hi - 1u);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const uint32_t v = __float_as_uint(fmaf(vh, 0.25f * (u + 1), vl * (0.75f - 0.25f * u)));
+      mid[u] = max(min((v ^ (uint32_t(int(v) >> 31) | 0x80000000u)) + 1u, hi - 1u), lo + 1u);
+    }
+    mid[1] = max(mid[1], mid[0]);
+    mid[2] = max(mid[2], mid[1]);
+  } else {
+    const uint32_t quarter = (hi - lo) / 4u;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) mid[u] = min(lo + max(quarter * (u + 1), 1u), hi - 1u);
+  }
+}
+
 // Builds the ordered block list [t, I_t...] of one query block in shared
 // memory with each block's log2-domain gate. Run by one warp.
 __device__ __forceinline__ void build_block_list(const int32_t* __restrict__ idx_row, int K, int t,

@@ -216,12 +216,12 @@ struct Query {
 
 // A warp's running state. Rows of `acc` are channels: acc[j][i] holds channel
 // 32 j + 4 g + 2 i (elements 0, 1) and 16 times the one after it (elements 2,
-// 3) of heads 2t (even elements) and 2t + 1. Each nibble is masked out for a
-// row of its own. Whole bytes (x + 16 y, with x taken out of the difference at
-// the end) save an AND of 700 instructions' 32 and 3 % of the time, but the
-// tensor cores truncate their sums, and the difference has 17 times that error:
-// over all 2048 blocks of a row, whose outputs are small next to Σ p s code, it
-// cost a bit of the output.
+// 3) of heads 2t (even elements) and 2t + 1. Every nibble is masked out for a
+// row of its own. Whole bytes (x + 16 y, with x as the difference of two rows)
+// save an AND per word, 44.9 us against 45.6 over the 2048 blocks of a row. But
+// the tensor cores cut their sums off, and x has 17 times that error: on this
+// row, whose outputs are small next to Σ p s code, o was off by 0.32 % against
+// 0.17 %, the rounding to bf16.
 template <int D>
 struct State {
   static constexpr int NG = D / kGroup;
@@ -636,18 +636,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// The score that has an orderable key.
-__device__ __forceinline__ float key_score(uint32_t k) {
-  return __uint_as_float(k ^ (uint32_t(int(~k) >> 31) | 0x80000000u));
-}
-
 // One warp's Top-K of a score row, without a block-wide barrier: lane i holds
 // the keys of blocks i, 32 + i, ... in registers. A bisection between the
 // smallest and the largest key finds a threshold with n keys at or above it, in
-// half a dozen counts of the row: each step quarters the range, at first that
-// of the values, which spread evenly over their own range, and after 8 steps
-// that of the keys, which ends for sure. Where a tie is cut, it ends on the
-// tied key.
+// half a dozen counts of the row (quarter_keys). Where a tie is cut, it ends on
+// the tied key.
 template <int CAP>
 struct Row {
   uint32_t key[CAP];  // orderable key + 1, 0 past the history
@@ -698,22 +691,8 @@ struct Row {
           need = n - above;
           break;
         }
-        // three keys in (lo, hi), in ascending order (equal ones do no harm)
         uint32_t mid[3];
-        if (round < 8) {
-          const float vl = key_score(lo - 1u), vh = key_score(hi - 1u);
-#pragma unroll
-          for (int u = 0; u < 3; ++u) {
-            const uint32_t v = __float_as_uint(fmaf(vh, 0.25f * (u + 1), vl * (0.75f - 0.25f * u)));
-            mid[u] = max(min((v ^ (uint32_t(int(v) >> 31) | 0x80000000u)) + 1u, hi - 1u), lo + 1u);
-          }
-          mid[1] = max(mid[1], mid[0]);
-          mid[2] = max(mid[2], mid[1]);
-        } else {
-          const uint32_t quarter = (hi - lo) / 4u;
-#pragma unroll
-          for (int u = 0; u < 3; ++u) mid[u] = min(lo + max(quarter * (u + 1), 1u), hi - 1u);
-        }
+        quarter_keys(lo, hi, round, mid);
         int cnt[3] = {0, 0, 0};
 #pragma unroll
         for (int i = 0; i < CAP; ++i)
