@@ -11,10 +11,9 @@
 // Read: bf16(s·code + m), one rounding. Means: (1/64) Σ (s·code + m) in fp32.
 //
 // The read is bound by the bytes it moves, write and means by the integer pipe
-// as well. Write and read give a tile of 16
-// tokens to a warp, the means a record: enough independent 16-byte loads per
-// lane that the few dependent ones before them (length, page) are hidden by the
-// other warps of the multiprocessor.
+// as well. Write and read give a tile of 16 tokens to a warp, the means a
+// record: enough independent 16-byte loads per lane that the few dependent ones
+// before them (length, page) are hidden by the multiprocessor's other warps.
 #include "kv4.cuh"
 
 namespace sas {
