@@ -289,6 +289,10 @@ __device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& 
 
 // The online softmax: S becomes p · 2^-20 with p = 2^(S f + lam - max), and the
 // state is rescaled. (f > 0, so the largest logit is that of the largest S.)
+// Every S is taken relative to the block's largest before it is scaled: p is
+// then at most 1 whatever the logits' size, as the range of fp16 needs it, and
+// a token is weighed by its distance from the largest, not by a difference of
+// two roundings of large numbers.
 template <int D, int NT>
 __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[NT][2]) {
   float top[2], sub[2], al[2];
@@ -306,19 +310,22 @@ __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, f
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float mx = fmaxf(st.m[h], fmaf(top[h], h ? q.f.y : q.f.x, lam));
+    const float own = fmaf(top[h], h ? q.f.y : q.f.x, lam);  // the block's largest logit
+    const float mx = fmaxf(st.m[h], own);
     const float ref = mx == -INFINITY ? 0.f : mx;  // nothing but masked tokens so far: every p is 0
     al[h] = exp2_approx(st.m[h] - ref);
-    sub[h] = lam - ref + kPShift;
+    sub[h] = (own - ref) + kPShift;
+    top[h] = top[h] == -INFINITY ? 0.f : -top[h];
     st.m[h] = mx;
   }
+  const float2 less = make_float2(top[0], top[1]);
   const float2 add = make_float2(sub[0], sub[1]);
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float2 z = fma_f32x2(S[i][u], q.f, add);
+      float2 z = fma_f32x2(add_f32x2(S[i][u], less), q.f, add);
       z.x = exp2_approx(z.x);
       z.y = exp2_approx(z.y);
       S[i][u] = z;
