@@ -424,7 +424,9 @@ SAS_API sas_status sas_kv4_block_mean_keys(const sas_params* p, const sas_kv4_ca
 /* sas_decode over the 4-bit cache, dense or paged: the same block list, gate
  * modes, splits and outputs, merged by sas_decode_combine. The cache's values
  * s·code + m enter the products unrounded. The logits are exact to fp32; P and
- * P·s are rounded to 11 bits for P·V. A V step under 2^-16 of the largest one
+ * P·s are rounded to 11 bits for P·V. A P under 2^-22 of the row's largest (with
+ * SAS_GATE_SOFTMAX_OUTSIDE: of its largest P·g) has fewer bits, and under 2^-33
+ * only its minima's part counts. A V step under 2^-16 of the largest one
  * of the row is not resolved there, which moves an output by less than 2^-13 of
  * that largest step. A NaN group of K makes the row NaN, one of V its 32
  * channels. n_pages · Hkv is at most 2^25. */

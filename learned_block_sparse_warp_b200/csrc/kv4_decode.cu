@@ -60,7 +60,7 @@ struct Kv4DecodeArgs {
   uint16_t* o;             // one-launch form
   float* lse_o;            // may be null
   int* err;
-  int B, Hkv, G, Lmax, K, gate, gated, outside, n_split;
+  int B, Hkv, G, Lmax, K, gate, gated, n_split;
   float scale;
 };
 
@@ -228,6 +228,7 @@ struct State {
   float acc[NG][2][4];
   float2 accm[NG];    // Σ p m over this lane's tokens, heads 2t and 2t + 1
   float m[2], l[2];   // maximum (log2), and Σ p over this lane's tokens (p times 2^-20 throughout)
+  float w[2];         // gate outside the softmax: acc and accm are to be multiplied by 2^w
   uint32_t lo;        // base of the steps' exponent field, as bf16 bits in both halves
   uint32_t lim;       // largest step bits below the limit, in both halves
 
@@ -240,6 +241,7 @@ struct State {
     }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
+    w[0] = w[1] = -INFINITY;
     lo = lim = 0u;
   }
 };
@@ -289,13 +291,19 @@ __device__ __forceinline__ void score_block(const uint8_t* rec, const Query<D>& 
 
 // The online softmax: S becomes p · 2^-20 with p = 2^(S f + lam - max), and the
 // state is rescaled. (f > 0, so the largest logit is that of the largest S.)
+//
+// With OUT the gate lies outside the softmax: the sum is over 2^(S f - max), and
+// S becomes 2^(S f - max + lam - w). The weights have a running maximum 2^w of
+// their own, relative to the softmax's, because P has fp16's range and a row's
+// mass may lie where its gates are small, or a caller's LSE make them large.
+//
 // Every S is taken relative to the block's largest before it is scaled: p is
 // then at most 1 whatever the logits' size, as the range of fp16 needs it, and
 // a token is weighed by its distance from the largest, not by a difference of
 // two roundings of large numbers.
-template <int D, int NT>
+template <int D, int NT, bool OUT>
 __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, float lam, float2 (&S)[NT][2]) {
-  float top[2], sub[2], al[2];
+  float top[2], sub[2], al[2], out_sub[2], out_al[2];
   top[0] = fmaxf(S[0][0].x, S[0][1].x);
   top[1] = fmaxf(S[0][0].y, S[0][1].y);
 #pragma unroll
@@ -310,39 +318,55 @@ __device__ __forceinline__ void softmax_block(State<D>& st, const Query<D>& q, f
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float own = fmaf(top[h], h ? q.f.y : q.f.x, lam);  // the block's largest logit
+    const float own = fmaf(top[h], h ? q.f.y : q.f.x, OUT ? 0.f : lam);  // the block's largest logit
     const float mx = fmaxf(st.m[h], own);
     const float ref = mx == -INFINITY ? 0.f : mx;  // nothing but masked tokens so far: every p is 0
     al[h] = exp2_approx(st.m[h] - ref);
     sub[h] = (own - ref) + kPShift;
+    if (OUT) {
+      const float was = st.w[h] + (st.m[h] - ref), here = (own - ref) + lam;
+      st.w[h] = fmaxf(was, here);
+      const float wref = st.w[h] == -INFINITY ? 0.f : st.w[h];
+      out_al[h] = exp2_approx(was - wref);
+      out_sub[h] = (here - wref) + kPShift;
+    } else {
+      out_al[h] = al[h];
+    }
     top[h] = top[h] == -INFINITY ? 0.f : -top[h];
     st.m[h] = mx;
   }
   const float2 less = make_float2(top[0], top[1]);
   const float2 add = make_float2(sub[0], sub[1]);
+  const float2 out_add = OUT ? make_float2(out_sub[0], out_sub[1]) : add;
   float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float2 z = fma_f32x2(add_f32x2(S[i][u], less), q.f, add);
+      const float2 d = add_f32x2(S[i][u], less);
+      float2 z = fma_f32x2(d, q.f, add);
       z.x = exp2_approx(z.x);
       z.y = exp2_approx(z.y);
-      S[i][u] = z;
       sum = add_f32x2(sum, z);
+      if (OUT) {
+        z = fma_f32x2(d, q.f, out_add);
+        z.x = exp2_approx(z.x);
+        z.y = exp2_approx(z.y);
+      }
+      S[i][u] = z;
     }
   st.l[0] = fmaf(st.l[0], al[0], sum.x);
   st.l[1] = fmaf(st.l[1], al[1], sum.y);
-  if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+  if (__any_sync(0xffffffffu, out_al[0] != 1.f || out_al[1] != 1.f)) {
 #pragma unroll
     for (int j = 0; j < State<D>::NG; ++j) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        st.acc[j][0][e] *= al[e & 1];
-        st.acc[j][1][e] *= al[e & 1];
+        st.acc[j][0][e] *= out_al[e & 1];
+        st.acc[j][1][e] *= out_al[e & 1];
       }
-      st.accm[j].x *= al[0];
-      st.accm[j].y *= al[1];
+      st.accm[j].x *= out_al[0];
+      st.accm[j].y *= out_al[1];
     }
   }
 }
@@ -457,23 +481,18 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void weigh(float2& p, float w) {
-  p.x *= w;
-  p.y *= w;
-}
-
 // A warp over its n blocks: records rec_s, gates lam_s (log2). The first block
 // has ntok0 tokens, the others all. Both items of the first are under way. A
 // block that is not full goes through a loop of single tiles, which keeps the
 // code that a warp has to fetch small.
-template <int D>
+template <int D, bool OUT>
 __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st, const Query<D>& q, uint8_t* ring,
                                            const int* rec_s, const float* lam_s, int n, int ntok0) {
   using R = Ring<D>;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int ntok = rec_s[i] < 0 ? 0 : i == 0 ? ntok0 : kBlock;
-    const float lam = a.gated ? lam_s[i] : 0.f, bias = a.outside ? 0.f : lam;
+    const float lam = a.gated ? lam_s[i] : 0.f;
     if (ntok == kBlock) {
       float2 S[kTiles][2];
       cp_async_wait<1>();
@@ -481,12 +500,7 @@ __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st,
       score_block<D, kTiles, true>(ring, q, ntok, S);
       __syncwarp();
       R::step(ring, a.c, rec_s, n, ntok0, 2 * i + 2);
-      softmax_block<D, kTiles>(st, q, bias, S);
-      if (a.outside) {
-        const float gw = exp2f(lam);
-#pragma unroll
-        for (int k = 0; k < kTiles; ++k) weigh(S[k][0], gw), weigh(S[k][1], gw);
-      }
+      softmax_block<D, kTiles, OUT>(st, q, lam, S);
       cp_async_wait<1>();
       __syncwarp();
       value_block<D, kTiles, true>(ring + R::kRecord, st, ntok, S);
@@ -498,8 +512,7 @@ __device__ __forceinline__ void run_blocks(const Kv4DecodeArgs& a, State<D>& st,
         float2 S[1][2];
         const uint8_t* tile = ring + k * Fmt<D>::kTileBytes;
         score_block<D, 1, false>(tile, q, ntok - k * kTile, S);
-        softmax_block<D, 1>(st, q, bias, S);
-        if (a.outside) weigh(S[0][0], exp2f(lam)), weigh(S[0][1], exp2f(lam));
+        softmax_block<D, 1, OUT>(st, q, lam, S);
         value_block<D, 1, false>(tile + R::kRecord, st, ntok - k * kTile, S);
       }
       __syncwarp();
@@ -530,7 +543,7 @@ struct Merge {
       : CS(CS), rank(rank), GS(lanes(CS)), U(G * NG * GS), o(reinterpret_cast<float4*>(smem)),
         ml(reinterpret_cast<float2*>(smem + CS * kWarps * U * 16)) {}
 
-  template <bool CLUSTER>
+  template <bool CLUSTER, bool OUT>
   __device__ __forceinline__ void push(State<D>& st, int G) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, from = rank * kWarps + int(threadIdx.x >> 5);
     // the minima's sums over the lanes g: lane g gets the total of one (group,
@@ -566,7 +579,9 @@ struct Merge {
       l[h] = st.l[h];
 #pragma unroll
       for (int x = 4; x <= 16; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-      const float inv = l[h] == 0.f ? 0.f : __fdividef(1.f, l[h]), f0 = inv * f, f1 = f0 * 0.0625f;
+      float inv = l[h] == 0.f ? 0.f : __fdividef(1.f, l[h]);
+      if (OUT) inv *= exp2_approx(st.w[h]);
+      const float f0 = inv * f, f1 = f0 * 0.0625f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         const int from_g = NG == 4 ? 2 * j + h : 2 * (2 * j + h);
@@ -760,7 +775,7 @@ struct Row {
 // of 168 in the one-launch form, whose registers the selection needs. Clusters
 // past one wave of CTAs cost more than they even out (128K 45.8 -> 52.9 us for
 // the step).
-template <int D, bool CLUSTER>
+template <int D, bool CLUSTER, bool OUT>
 __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4DecodeArgs a) {
   using R = Ring<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -810,15 +825,15 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
   q.make(raw, a.scale);
   State<D> st;
   st.clear();
-  run_blocks<D>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
+  run_blocks<D, OUT>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
   const Merge<D> mg(CLUSTER ? smem + kWarps * R::kBytes : smem, a.G, CS, rank);
   if (CLUSTER) {
     cluster_begun();
-    mg.template push<true>(st, a.G);
+    mg.template push<true, OUT>(st, a.G);
     cluster_sync();
   } else {
     __syncthreads();  // the rings are done with, and the partials take their place
-    mg.template push<false>(st, a.G);
+    mg.template push<false, OUT>(st, a.G);
     __syncthreads();
   }
   mg.run([&](int head, int col, float4 o, float lse) {
@@ -841,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
 // 8.8, the partials merged after 11.6. Selecting nothing would save 0.2 us, for
 // the rest is hidden by the other warps and the launches on either side.
 // Clusters of 16 for few rows are slower (9.8 -> 10.7 us).
-template <int D, int CAP>
+template <int D, int CAP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4DecodeArgs a) {
   using R = Ring<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -917,10 +932,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_decode_fused_kernel(Kv4Decode
     for (int i = lane; i < a.K; i += 32) a.idx_out[size_t(bh) * a.K + i] = i < n_pick ? sel_s[i] : -1;
   State<D> st;
   st.clear();
-  run_blocks<D>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
+  run_blocks<D, OUT>(a, st, q, ring, rec_s[warp], lam_s[warp], n, ntok0);
   const Merge<D> mg(smem + kWarps * R::kBytes, a.G, CS, rank);
   cluster_begun();
-  mg.template push<true>(st, a.G);
+  mg.template push<true, OUT>(st, a.G);
   cluster_sync();
   mg.run([&](int head, int col, float4 o, float ls) {
     const size_t at = size_t(bh) * a.G + head;
@@ -944,7 +959,6 @@ static Kv4DecodeArgs kv4_decode_args(const Shape& sh, const uint16_t* q, const C
   a.K = sh.K;
   a.gate = sh.gate;
   a.gated = sh.gated;
-  a.outside = sh.outside;
   a.scale = sh.scale;
   return a;
 }
@@ -981,7 +995,7 @@ static cudaError_t multiprocessors(int* sms) {
 // Split form. The cluster size: the largest power of two that keeps every CTA
 // resident at once (16 warps per SM), at most 8 and at most one warp per block
 // of a split.
-template <int D>
+template <int D, bool OUT>
 static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
   constexpr int ring = kWarps * Ring<D>::kBytes;
   int sms = 0;
@@ -991,8 +1005,8 @@ static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
   const int want = min(min(kMaxCluster, (per + kWarps - 1) / kWarps), sms * 4 / items);
   int cs = 1;
   while (cs * 2 <= want) cs *= 2;
-  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, false>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
-  return launch_ctas(kv4_decode_split_kernel<D, true>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, false, OUT>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
+  return launch_ctas(kv4_decode_split_kernel<D, true, OUT>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
 }
 
 cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl, const float* s,
@@ -1004,20 +1018,26 @@ cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c
   a.n_split = n_split;
   a.o_part = o_part;
   a.lse_part = lse_part;
-  return sh.d == 128 ? launch_split<128>(a, st) : launch_split<64>(a, st);
+  if (sh.outside) return sh.d == 128 ? launch_split<128, true>(a, st) : launch_split<64, true>(a, st);
+  return sh.d == 128 ? launch_split<128, false>(a, st) : launch_split<64, false>(a, st);
 }
 
 // One launch. The cluster size: as many CTAs per row as keep the grid in one
 // wave of resident CTAs, at most 8 and at most one warp per block of the list.
-template <int D, int CAP>
-static cudaError_t launch_fused(const Kv4DecodeArgs& a, cudaStream_t st) {
+template <int D, int CAP, bool OUT>
+static cudaError_t launch_fused_as(const Kv4DecodeArgs& a, cudaStream_t st) {
   constexpr int ring = kWarps * Ring<D>::kBytes;
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
   const int rows = a.B * a.Hkv;
   const int cs = max(1, min(min(kMaxCluster, (a.K + kWarps) / kWarps), sms * 3 / rows));
-  return launch_ctas(kv4_decode_fused_kernel<D, CAP>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  return launch_ctas(kv4_decode_fused_kernel<D, CAP, OUT>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+}
+
+template <int D, int CAP>
+static cudaError_t launch_fused(const Kv4DecodeArgs& a, bool outside, cudaStream_t st) {
+  return outside ? launch_fused_as<D, CAP, true>(a, st) : launch_fused_as<D, CAP, false>(a, st);
 }
 
 cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl,
@@ -1029,9 +1049,9 @@ cudaError_t launch_decode_fused_kv4(const Shape& sh, const uint16_t* q, const Ca
   a.o = o;
   a.lse_o = lse_o;
   // blocks of a row that the selecting warp's registers hold
-  if (sh.NB <= 4 * 32) return sh.d == 128 ? launch_fused<128, 4>(a, st) : launch_fused<64, 4>(a, st);
-  if (sh.NB <= 16 * 32) return sh.d == 128 ? launch_fused<128, 16>(a, st) : launch_fused<64, 16>(a, st);
-  return sh.d == 128 ? launch_fused<128, 64>(a, st) : launch_fused<64, 64>(a, st);
+  if (sh.NB <= 4 * 32) return sh.d == 128 ? launch_fused<128, 4>(a, sh.outside, st) : launch_fused<64, 4>(a, sh.outside, st);
+  if (sh.NB <= 16 * 32) return sh.d == 128 ? launch_fused<128, 16>(a, sh.outside, st) : launch_fused<64, 16>(a, sh.outside, st);
+  return sh.d == 128 ? launch_fused<128, 64>(a, sh.outside, st) : launch_fused<64, 64>(a, sh.outside, st);
 }
 
 }  // namespace sas
