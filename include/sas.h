@@ -78,7 +78,9 @@ typedef enum {
 
 typedef enum {
   /* Training form, Eq. (9): log g_m = s_m − LSE(s) is added to the logits of
-   * every token of selected history block m. The current block gets 0. */
+   * every token of selected history block m. The current block gets 0. A
+   * history whose scores are all −inf has every gate closed (g = 0), here and
+   * under SAS_GATE_SOFTMAX_OUTSIDE, and ds = 0. */
   SAS_GATE_LOG_SOFTMAX = 0,
   /* Inference form (Algorithm 2): Top-K selection only, no gate term. */
   SAS_GATE_NONE = 1,

@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(256) bwd_ds_chain_kernel(const float* __restri
     }
     sum = warp_sum(sum);
     const float lse = lse_s[r];
-    for (int m = lane; m < NB; m += 32) dsr[m] = (m < t) ? -expf(sr[m] - lse) * sum : 0.f;
+    const bool open = lse != -INFINITY;  // scores that are all −inf have no softmax, and every gate is 0
+    for (int m = lane; m < NB; m += 32) dsr[m] = (m < t && open) ? -expf(sr[m] - lse) * sum : 0.f;
   } else {  // log σ(s) and the raw logit act on each selected block alone
     for (int m = lane; m < NB; m += 32) dsr[m] = 0.f;
   }

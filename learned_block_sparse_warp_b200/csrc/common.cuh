@@ -29,11 +29,12 @@ struct Shape {
 
 // λ_m of a selected history block in log2 units, log g_m · log2 e, for the gate
 // mode: s_m − LSE(s) (softmax-normalised, inside or outside the softmax),
-// log σ(s_m), s_m (raw logit), or 0.
+// log σ(s_m), s_m (raw logit), or 0. A history whose scores are all −inf has
+// LSE(s) = −inf and no open gate.
 __device__ __forceinline__ float gate_lam2(int gate, float s_m, float lse) {
   switch (gate) {
     case SAS_GATE_LOG_SOFTMAX:
-    case SAS_GATE_SOFTMAX_OUTSIDE: return (s_m - lse) * kLog2e;
+    case SAS_GATE_SOFTMAX_OUTSIDE: return s_m == -INFINITY && lse == -INFINITY ? s_m : (s_m - lse) * kLog2e;
     case SAS_GATE_LOG_SIGMOID: return (fminf(s_m, 0.f) - log1pf(expf(-fabsf(s_m)))) * kLog2e;
     case SAS_GATE_LOGIT: return s_m * kLog2e;
     default: return 0.f;

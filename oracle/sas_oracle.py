@@ -176,6 +176,8 @@ def log_gate(s_hist: np.ndarray, selected: Sequence[int], gate_mode: int) -> np.
         return np.array([float(s_hist[m]) for m in selected], dtype=np.float64)
     # the softmax-normalised gate, inside (log g in the logits) or outside (g on the values)
     lse = logsumexp(s_hist)
+    if lse == -math.inf:  # scores that are all −inf: every gate is closed
+        return np.full(len(selected), -math.inf)
     return np.array([float(s_hist[m]) - lse for m in selected], dtype=np.float64)
 
 
@@ -189,7 +191,9 @@ def gate_score_gradient(s_hist: np.ndarray, selected: Sequence[int], dl_sel: np.
     sh = np.asarray(s_hist, np.float64)
     ds_row = np.zeros(len(sh))
     if gate_mode in (GATE_LOG_SOFTMAX, GATE_SOFTMAX_OUTSIDE):
-        ds_row = -np.exp(sh - logsumexp(sh)) * float(np.sum(dl_sel))
+        lse = logsumexp(sh)
+        if lse != -math.inf:
+            ds_row = -np.exp(sh - lse) * float(np.sum(dl_sel))
     for m, x in zip(selected, dl_sel):
         if gate_mode == GATE_LOG_SIGMOID:
             x = x * (1.0 - 1.0 / (1.0 + math.exp(-sh[m])))

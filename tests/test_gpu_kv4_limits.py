@@ -149,3 +149,37 @@ def test_outside_gate_under_another_rows_lse(shift, d):
     assert sas.sas_get_device_error() == 0
     worst = (np.abs(host(out["o"]).astype(np.float64) - ref) / tol).max()
     assert worst <= 1, f"{worst:.3g} of the bound"
+
+
+@pytest.mark.parametrize("form", ["fused", "split"])
+@pytest.mark.parametrize("gate", [O.GATE_LOG_SOFTMAX, O.GATE_LOG_SIGMOID, O.GATE_LOGIT, O.GATE_SOFTMAX_OUTSIDE])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_masked_history_leaves_the_current_block(d, gate, form):
+    """Scores that are all -inf close every gate, whatever its form: the current block alone is attended to, or with the
+    gate outside the softmax only its values count. The bound is _outside_bounds' with the picks' weights at 0."""
+    B, Hkv, T = 2, 2, 512
+    lens = [512, 300]
+    p = _params(B, 8, Hkv, d, T, 8, gate)
+    st = Store(p, True, seed=4, fill=0xFF)
+    k, v = _kv(B, Hkv, T, d, seed=13)
+    st.write(k, v, lens, lens)
+    st.handle()
+    q, s = _qs(p, seed=14)
+    s[:] = -np.inf
+    out = _run(p, st, q, lens, s, 3, form)
+    assert np.all(host(out["lse_s"]) == -np.inf)
+    o, lse = host(out["o"]).astype(np.float64), host(out["lse_o"]).astype(np.float64)
+    for b, L in enumerate(lens):
+        cur = np.arange(L) >= 64 * ((L - 1) // 64)
+        for hq in range(8):
+            (kk, ka), (vv, va) = _row(p, st, lens, b, hq // 4, s)
+            steps = KV._bf16_value(KV._raw(st.rows("v", b, hq // 4), "v")[1].reshape(T, -1)[:L])
+            qv = q[b, hq].astype(np.float64)
+            z = kk @ qv / np.sqrt(d)
+            dz = 2.0 ** -18 * (ka @ np.abs(qv)).max() / np.sqrt(d)
+            ref = O.logsumexp(z) if gate == O.GATE_SOFTMAX_OUTSIDE else O.logsumexp(z[cur])
+            w = np.exp(z - ref) * cur
+            assert abs(lse[b, hq] - ref) <= dz + 2.0 ** -20 * (1 + abs(ref))
+            tol = (2.0 ** -8 * np.abs(w @ vv) + (1.05 * 2.0 ** -10 + 2 * dz) * (w @ va)
+                   + (15 * L * 2.0 ** -33 * w.max() + 2.0 ** -13 * w.sum()) * steps.max())
+            assert np.all(np.abs(o[b, hq] - w @ vv) <= tol), (b, hq)
