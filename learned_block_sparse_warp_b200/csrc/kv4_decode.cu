@@ -536,8 +536,11 @@ struct Merge {
   float4* o;            // [warp of the cluster][head][group][lane g / CS]
   float2* ml;           // [warp of the cluster][8 heads]
 
-  static __host__ __device__ int lanes(int CS) { return (7 + CS) / CS; }
-  static __host__ __device__ int bytes(int G, int CS) { return CS * kWarps * (G * NG * lanes(CS) * 16 + 64); }
+  static __host__ __device__ constexpr int lanes(int CS) { return (7 + CS) / CS; }
+  static __host__ __device__ constexpr int bytes(int G, int CS) { return CS * kWarps * (G * NG * lanes(CS) * 16 + 64); }
+  static constexpr int max_bytes(int CS = kMaxCluster) {  // of G <= 8 and up to CS CTAs
+    return CS == 1 ? bytes(8, 1) : max_bytes(CS - 1) > bytes(8, CS) ? max_bytes(CS - 1) : bytes(8, CS);
+  }
 
   __device__ __forceinline__ Merge(uint8_t* smem, int G, int CS, int rank)
       : CS(CS), rank(rank), GS(lanes(CS)), U(G * NG * GS), o(reinterpret_cast<float4*>(smem)),
@@ -964,10 +967,12 @@ static Kv4DecodeArgs kv4_decode_args(const Shape& sh, const uint16_t* q, const C
 }
 
 // Launches `kern` on `items` clusters of cs CTAs, as a dependent launch. cs = 0:
-// plain CTAs.
-static cudaError_t launch_ctas(void (*kern)(Kv4DecodeArgs), int items, int cs, int smem, cudaStream_t st,
+// plain CTAs. The kernel's limit of dynamic shared memory belongs to the
+// function, not to the launch: it is one constant per kernel, because a smaller
+// one set by another thread's call would refuse this one.
+static cudaError_t launch_ctas(void (*kern)(Kv4DecodeArgs), int items, int cs, int smem, int max_smem, cudaStream_t st,
                                const Kv4DecodeArgs& a) {
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(items) * max(cs, 1));
@@ -997,7 +1002,7 @@ static cudaError_t multiprocessors(int* sms) {
 // of a split.
 template <int D, bool OUT>
 static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int ring = kWarps * Ring<D>::kBytes;
+  constexpr int ring = kWarps * Ring<D>::kBytes, max_smem = ring + Merge<D>::max_bytes();
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
@@ -1005,8 +1010,8 @@ static cudaError_t launch_split(const Kv4DecodeArgs& a, cudaStream_t st) {
   const int want = min(min(kMaxCluster, (per + kWarps - 1) / kWarps), sms * 4 / items);
   int cs = 1;
   while (cs * 2 <= want) cs *= 2;
-  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, false, OUT>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), st, a);
-  return launch_ctas(kv4_decode_split_kernel<D, true, OUT>, items, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  if (cs == 1) return launch_ctas(kv4_decode_split_kernel<D, false, OUT>, items, 0, max(ring, Merge<D>::bytes(a.G, 1)), max_smem, st, a);
+  return launch_ctas(kv4_decode_split_kernel<D, true, OUT>, items, cs, ring + Merge<D>::bytes(a.G, cs), max_smem, st, a);
 }
 
 cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c, const int32_t* cl, const float* s,
@@ -1026,13 +1031,13 @@ cudaError_t launch_decode_kv4(const Shape& sh, const uint16_t* q, const Cache& c
 // wave of resident CTAs, at most 8 and at most one warp per block of the list.
 template <int D, int CAP, bool OUT>
 static cudaError_t launch_fused_as(const Kv4DecodeArgs& a, cudaStream_t st) {
-  constexpr int ring = kWarps * Ring<D>::kBytes;
+  constexpr int ring = kWarps * Ring<D>::kBytes, max_smem = ring + Merge<D>::max_bytes();
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
   const int rows = a.B * a.Hkv;
   const int cs = max(1, min(min(kMaxCluster, (a.K + kWarps) / kWarps), sms * 3 / rows));
-  return launch_ctas(kv4_decode_fused_kernel<D, CAP, OUT>, rows, cs, ring + Merge<D>::bytes(a.G, cs), st, a);
+  return launch_ctas(kv4_decode_fused_kernel<D, CAP, OUT>, rows, cs, ring + Merge<D>::bytes(a.G, cs), max_smem, st, a);
 }
 
 template <int D, int CAP>

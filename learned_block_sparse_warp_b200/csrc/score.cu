@@ -452,8 +452,9 @@ template <int D>
 static cudaError_t launch_scored_d(const ScoredSelectArgs& a, int rows, int C, cudaStream_t st) {
   const int slice = (a.NB - 1 + C - 1) / C;
   const size_t smem = size_t(slice > 0 ? slice : 1) * sizeof(float);
+  // one constant: the limit is the function's, and another thread's launch may come in between
   cudaError_t e = cudaFuncSetAttribute(select_scored_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(smem));
+                                       ssc::kMaxSlice * int(sizeof(float)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(rows * C);
