@@ -438,32 +438,58 @@ class Kv4Cache:
     """A 4-bit KV cache over the caller's uint8 tensors (the format is in include/sas.h).
 
     Dense: k and v are [B, Hkv, NKB, 40 d]. Paged: [n_pages, Hkv, 40 d], with block_table int32 [B, NKB]. The handle
-    keeps the tensors alive and may be used with any ``Params`` of the same batch, KV heads, head_dim and seq_len."""
+    keeps the tensors alive and may be used with any ``Params`` of the same batch, KV heads, head_dim and seq_len.
 
-    __slots__ = ("k", "v", "block_table", "dims", "device", "_c", "_ref")
+    ``block_table`` of a paged cache can be assigned, and later calls go by the new table; k, v and the shape stay.
+    Tensors whose memory has moved since (resized in place) are checked again and followed. A captured step keeps the
+    memory it was captured with."""
+
+    __slots__ = ("_k", "_v", "_block_table", "_dims", "_blocks", "_device", "_at", "_ref")
 
     def __init__(self, p: Params, k: torch.Tensor, v: torch.Tensor, block_table: Optional[torch.Tensor] = None):
-        n_pages = 0
-        shape = (p.batch, p.n_kv_heads, p.n_blocks, kv4_record_bytes(p.head_dim))
-        if block_table is not None:
-            n_pages = int(k.shape[0])
-            shape = (n_pages, p.n_kv_heads, kv4_record_bytes(p.head_dim))
-        dev = k.get_device()
-        if dev < 0:
+        if k is None:
+            raise ValueError("k: missing")
+        self._dims, self._blocks = (p.batch, p.n_kv_heads, p.head_dim, p.seq_len), p.n_blocks
+        self._device = k.get_device()
+        if self._device < 0:
             raise ValueError("k: expected a CUDA tensor")
-        self.k, self.v, self.block_table, self.device = k, v, block_table, dev
-        self.dims = (p.batch, p.n_kv_heads, p.head_dim, p.seq_len)
-        self._c = sas_kv4_cache(_arg(k, torch.uint8, shape, "k", dev), _arg(v, torch.uint8, shape, "v", dev),
-                                _opt(block_table, i32, (p.batch, p.n_blocks), "block_table", dev), n_pages)
-        self._ref = ctypes.byref(self._c)
+        self._bind(k, v, block_table)
+
+    def _bind(self, k, v, block_table) -> None:
+        B, Hkv, d, _ = self._dims
+        dev, n_pages = self._device, 0 if block_table is None else int(k.shape[0])
+        shape = ((B, Hkv, self._blocks) if block_table is None else (n_pages, Hkv)) + (kv4_record_bytes(d),)
+        at = (_arg(k, torch.uint8, shape, "k", dev), _arg(v, torch.uint8, shape, "v", dev),
+              _opt(block_table, i32, (B, self._blocks), "block_table", dev))
+        # a struct of its own: a call on another thread may be using the last one
+        self._k, self._v, self._block_table, self._at = k, v, block_table, at
+        self._ref = ctypes.byref(sas_kv4_cache(*at, n_pages))
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    dims = property(lambda self: self._dims)
+    device = property(lambda self: self._device)
+
+    @property
+    def block_table(self) -> Optional[torch.Tensor]:
+        return self._block_table
+
+    @block_table.setter
+    def block_table(self, table: Optional[torch.Tensor]) -> None:
+        if (table is None) != (self._block_table is None):
+            raise ValueError("block_table: a cache stays dense or paged")
+        self._bind(self._k, self._v, table)
 
     def of(self, p: Params):
         """(C struct, shapes of p), once p has been checked against the cache's shape and the current device."""
         sh = _Kv4Shapes.of(p)
-        if self.dims != sh.cache:
-            raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self.dims}, called with {sh.cache}")
-        if self.device != _device():
-            raise ValueError(f"cache: lies on cuda:{self.device}, the current device is cuda:{_device()}")
+        if self._dims != sh.cache:
+            raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self._dims}, called with {sh.cache}")
+        if self._device != _device():
+            raise ValueError(f"cache: lies on cuda:{self._device}, the current device is cuda:{_device()}")
+        t = self._block_table
+        if (self._k.data_ptr(), self._v.data_ptr(), None if t is None else t.data_ptr()) != self._at:
+            self._bind(self._k, self._v, t)
         return self._ref, sh
 
 
@@ -490,7 +516,7 @@ def _tokens(t, name: str) -> int:
 def sas_kv4_write(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
     """Quantises k, v [B, Hkv, T, d] into the cache at positions cache_len - new_len .. cache_len - 1 (new_len: T)."""
     ref, sh = cache.of(p)
-    dev, T = cache.device, _tokens(k, "k")
+    dev, T = cache._device, _tokens(k, "k")
     kv = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_write", lib.sas_kv4_write(
         sh.c, ref, T, _arg(k, bf16, kv, "k", dev), _arg(v, bf16, kv, "v", dev),
@@ -503,7 +529,7 @@ def sas_kv4_read(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stre
     ref, sh = cache.of(p)
     if k is None and v is None:
         raise ValueError("k, v: at least one output is needed")
-    dev, T = cache.device, _tokens(v, "v") if k is None else _tokens(k, "k")
+    dev, T = cache._device, _tokens(v, "v") if k is None else _tokens(k, "k")
     kv = (p.batch, p.n_kv_heads, T, p.head_dim)
     _check("sas_kv4_read", lib.sas_kv4_read(
         sh.c, ref, T, _opt(k, bf16, kv, "k", dev), _opt(v, bf16, kv, "v", dev),
@@ -515,7 +541,7 @@ def sas_kv4_block_mean_keys(p: Params, cache: Kv4Cache, n_tokens: int, cache_len
                             stream=None) -> None:
     """Block means of the blocks that the last new_len (default n_tokens) tokens completed, into kmean [B, Hkv, NKB, d]."""
     ref, sh = cache.of(p)
-    dev = cache.device
+    dev = cache._device
     _check("sas_kv4_block_mean_keys", lib.sas_kv4_block_mean_keys(
         sh.c, ref, n_tokens, _arg(cache_len, i32, sh.lens, "cache_len", dev),
         _opt(new_len, i32, sh.lens, "new_len", dev), _arg(kmean, bf16, sh.kmean, "kmean", dev), _stream_on(dev, stream)))
@@ -525,7 +551,7 @@ def sas_decode_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, idx, lse_s, n_sp
                    stream=None) -> None:
     """sas_decode over a 4-bit cache."""
     ref, sh = cache.of(p)
-    dev = cache.device
+    dev = cache._device
     B, Hq, d = sh.q
     _check("sas_decode_kv4", lib.sas_decode_kv4(
         sh.c, _arg(q, bf16, sh.q, "q", dev), ref, _arg(cache_len, i32, sh.lens, "cache_len", dev),
@@ -538,7 +564,7 @@ def sas_decode_fused_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, o, idx=Non
                          stream=None) -> None:
     """sas_decode_fused over a 4-bit cache: select, attention and merge in one launch."""
     ref, sh = cache.of(p)
-    dev = cache.device
+    dev = cache._device
     _check("sas_decode_fused_kv4", lib.sas_decode_fused_kv4(
         sh.c, _arg(q, bf16, sh.q, "q", dev), ref, _arg(cache_len, i32, sh.lens, "cache_len", dev),
         _arg(s, f32, sh.s, "s", dev), _opt(idx, i32, sh.idx, "idx", dev), _opt(lse_s, f32, sh.lse_s, "lse_s", dev),
@@ -649,7 +675,7 @@ def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: d
     """Select, split-K attention and merge over a 4-bit cache, every argument checked once and before the first
     launch. select(c, pointers..., stream) launches the selection."""
     ref, sh = cache.of(p)
-    dev, c, st = cache.device, sh.c, _stream_on(cache.device, stream)
+    dev, c, st = cache._device, sh.c, _stream_on(cache._device, stream)
     B, Hq, d = sh.q
     qp, lp = _arg(q, bf16, sh.q, "q", dev), _arg(cache_len, i32, sh.lens, "cache_len", dev)
     sp = _arg(s, f32, sh.s, "s", dev)
@@ -685,7 +711,7 @@ def decode_step_scored_kv4(p: Params, q, k_new, v_new, cache: Kv4Cache, kmean, c
     select in one launch (s is written), split-K attention, merge."""
     if _tokens(k_new, "k_new") != 1:
         raise ValueError(f"k_new: expected one token, got {k_new.shape[2]}")
-    kp = _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", cache.device)
+    kp = _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", cache._device)
 
     def select(c, qp, lp, sp, ip, ep, st):
         sas_kv4_write(p, cache, k_new, v_new, cache_len, stream=stream)
@@ -732,6 +758,8 @@ class DecodeGraph:
             self.step, self.args = decode_step_fused_kv4, (p, q, cache, cache_len, s, out)
         else:
             self.step, self.args = decode_step_kv4, (p, q, cache, cache_len, s, n_split, out)
+        # what the captured pointers point to, whatever the cache and out hold later
+        self.memory = (cache.k, cache.v, cache.block_table, *out.values())
         self._capture(stream)
         return self
 
