@@ -671,9 +671,21 @@ def decode_step_scored(p: Params, q, kc, vc, kmean, cache_len, s, n_split: int, 
     sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
 
 
-def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream) -> None:
+def _refuse_decode_kv4(p: Params, n_split: int, pointers) -> None:
+    """The rules of sas_decode_kv4 and of alignment, for steps that change something before that call."""
+    code = 0
+    if p.n_q_heads > 8 * p.n_kv_heads:
+        code = 2  # SAS_ERR_UNSUPPORTED
+    elif any(x & 15 for x in pointers) or not 1 <= n_split <= min(p.top_k + 1, 65535):
+        code = 1  # SAS_ERR_INVALID_ARG
+    elif (p.top_k + n_split) // n_split > 64 or p.batch * p.n_kv_heads * n_split >= 1 << 31:
+        code = 2
+    _check("sas_decode_kv4", code)
+
+
+def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream, more=()) -> None:
     """Select, split-K attention and merge over a 4-bit cache, every argument checked once and before the first
-    launch. select(c, pointers..., stream) launches the selection."""
+    launch. select(c, cache, pointers..., stream) launches the selection, which takes the pointers `more` too."""
     ref, sh = cache.of(p)
     dev, c, st = cache._device, sh.c, _stream_on(cache._device, stream)
     B, Hq, d = sh.q
@@ -684,14 +696,15 @@ def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: d
     op = _arg(out["o_part"], f32, (B, Hq, n_split, d), "o_part", dev)
     xp = _arg(out["lse_part"], f32, (B, Hq, n_split), "lse_part", dev)
     yp, zp = _arg(out["o"], bf16, sh.q, "o", dev), _opt(out.get("lse_o"), f32, sh.lse_o, "lse_o", dev)
-    select(c, qp, lp, sp, ip, ep, st)
+    _refuse_decode_kv4(p, n_split, (qp, lp, sp, ip, ep, op, xp, yp, zp or 0, *more))
+    select(c, ref, qp, lp, sp, ip, ep, st)
     _check("sas_decode_kv4", lib.sas_decode_kv4(c, qp, ref, lp, sp, ip, ep, n_split, op, xp, st))
     _check("sas_decode_combine", lib.sas_decode_combine(c, n_split, op, xp, yp, zp, st))
 
 
 def decode_step_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, stream=None) -> None:
     """One decode step over a 4-bit cache: Top-K select (decode form), split-K attention, LSE merge."""
-    def select(c, qp, lp, sp, ip, ep, st):
+    def select(c, ref, qp, lp, sp, ip, ep, st):
         _check("sas_topk_select", lib.sas_topk_select(c, sp, lp, ip, ep, st))
 
     _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream)
@@ -711,14 +724,18 @@ def decode_step_scored_kv4(p: Params, q, k_new, v_new, cache: Kv4Cache, kmean, c
     select in one launch (s is written), split-K attention, merge."""
     if _tokens(k_new, "k_new") != 1:
         raise ValueError(f"k_new: expected one token, got {k_new.shape[2]}")
-    kp = _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", cache._device)
+    if (p.n_blocks + 6) // 8 > 53248:  # rows of scores past a cluster's shared memory
+        _check("sas_decode_select_scored", 2)
+    dev, one = cache._device, (p.batch, p.n_kv_heads, 1, p.head_dim)
+    new_k, new_v = _arg(k_new, bf16, one, "k_new", dev), _arg(v_new, bf16, one, "v_new", dev)
+    kp = _arg(kmean, bf16, (p.batch, p.n_kv_heads, p.n_blocks, p.head_dim), "kmean", dev)
 
-    def select(c, qp, lp, sp, ip, ep, st):
-        sas_kv4_write(p, cache, k_new, v_new, cache_len, stream=stream)
-        sas_kv4_block_mean_keys(p, cache, 1, cache_len, kmean, stream=stream)
+    def select(c, ref, qp, lp, sp, ip, ep, st):
+        _check("sas_kv4_write", lib.sas_kv4_write(c, ref, 1, new_k, new_v, lp, None, st))
+        _check("sas_kv4_block_mean_keys", lib.sas_kv4_block_mean_keys(c, ref, 1, lp, None, kp, st))
         _check("sas_decode_select_scored", lib.sas_decode_select_scored(c, qp, kp, lp, sp, ip, ep, st))
 
-    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream)
+    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream, (new_k, new_v, kp))
 
 
 class DecodeGraph:

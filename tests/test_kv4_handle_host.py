@@ -16,6 +16,9 @@ class Fake:
     def get_device(self):
         return self.dev
 
+    def dim(self):
+        return len(self.shape)
+
     def is_contiguous(self):
         return True
 
