@@ -767,6 +767,10 @@ class DecodeGraph:
             k_new=None, v_new=None, fused: bool = False) -> "DecodeGraph":
         """The same over a 4-bit cache: ``decode_step_kv4``, ``decode_step_fused_kv4`` (fused), or with kmean, k_new and
         v_new ``decode_step_scored_kv4``. The capture runs the step once: a scored step writes its token then."""
+        if len({kmean is None, k_new is None, v_new is None}) > 1:
+            raise ValueError("kmean, k_new, v_new: a scored step takes all three, another none")
+        if fused and kmean is not None:
+            raise ValueError("fused: a scored step is made of separate launches")
         self = cls.__new__(cls)
         if kmean is not None:
             self.step = decode_step_scored_kv4

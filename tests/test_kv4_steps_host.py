@@ -1,5 +1,7 @@
 """What the 4-bit cache's steps refuse, on the CPU: nothing may have been launched by then, for a step writes the cache, the
 means and the scores before its attention. The library is replaced by a recorder, and the codes are the C entry's own."""
+import types
+
 import pytest
 import torch
 
@@ -100,3 +102,11 @@ def test_the_codes_are_the_c_entrys(kw, code):
 def test_rows_of_scores_past_a_clusters_memory():
     p = sas.Params(batch=1, n_q_heads=1, n_kv_heads=1, head_dim=128, seq_len=64 * (8 * 53248 + 2), top_k=4)
     assert sas.lib.sas_decode_select_scored(p.c(), A, A, A, A, A, A, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(k_new=1), dict(v_new=1), dict(kmean=1), dict(k_new=1, v_new=1), dict(kmean=1, k_new=1),
+                                dict(kmean=1, k_new=1, v_new=1, fused=True)])
+def test_a_captured_step_is_one_of_the_three(kw):
+    cache = types.SimpleNamespace(k=None, v=None, block_table=None)
+    with pytest.raises(ValueError, match="scored step"):
+        sas.DecodeGraph.kv4(None, None, cache, None, None, 1, {}, **kw)
