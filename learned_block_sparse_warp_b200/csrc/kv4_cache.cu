@@ -52,6 +52,10 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 // goes up, as in the definition. fma adds 1.5·2^23, so the code is in the low
 // bits, rounded once. A value just under half-way may have gone up with them:
 // its residue x − m − s·code is below −s/2, and such a code is taken down.
+// x − m and the residue are rounded down. What they are compared with, half an
+// odd multiple of s, is an fp32 number, so a difference that is not one (of
+// values of very different sizes) stays on its side of it, and the codes are
+// those of the exact x − m.
 __device__ __forceinline__ Quant16 quantise16(const uint4 (&x)[2]) {
   constexpr float kMagic = 12582912.f;
   const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -91,9 +95,9 @@ __device__ __forceinline__ Quant16 quantise16(const uint4 (&x)[2]) {
     uint32_t word = 0;
 #pragma unroll
     for (int i = 4 * h + 3; i >= 4 * h; --i) {
-      const float2 d = add_f32x2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), dup2(neg_lo));
+      const float2 d = add_down_f32x2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), dup2(neg_lo));
       const float2 c = fma_f32x2(d, dup2(r), dup2(kMagic));
-      const float2 rest = fma_f32x2(add_f32x2(c, dup2(-kMagic)), dup2(-s), d);
+      const float2 rest = fma_down_f32x2(add_f32x2(c, dup2(-kMagic)), dup2(-s), d);
       least = min3(least, rest.x, rest.y);
       word = word * 16u + __float_as_uint(c.y);
       word = word * 16u + __float_as_uint(c.x);
@@ -108,9 +112,9 @@ __device__ __forceinline__ Quant16 quantise16(const uint4 (&x)[2]) {
       for (int i = 4 * h + 3; i >= 4 * h; --i)
 #pragma unroll
         for (int e = 1; e >= 0; --e) {
-          const float d = __fadd_rn(__uint_as_float(e ? w[i] & 0xffff0000u : w[i] << 16), neg_lo);
+          const float d = __fadd_rd(__uint_as_float(e ? w[i] & 0xffff0000u : w[i] << 16), neg_lo);
           const float n = fmaf(d, r, kMagic) - kMagic;
-          word = (word << 4) | (uint32_t(n) - (fmaf(n, -s, d) < -0.5f * s ? 1u : 0u));
+          word = (word << 4) | (uint32_t(n) - (__fmaf_rd(n, -s, d) < -0.5f * s ? 1u : 0u));
         }
       q.word[h] = word;
     }

@@ -6,7 +6,8 @@ values that ``unpack`` returns.
 
 A group is 32 channels of one token. m = min, s = bf16((max − min) / 15) with
 the difference and the quotient in fp32, 0 below 2^-126, and
-code = floor((x − m) / s + 1/2). A group whose range is not a finite fp32
+code = floor((x − m) / s + 1/2), exactly: the number of half-way points
+(k + 1/2) s that x − m reaches. A group whose range is not a finite fp32
 number is kept as s = 0, m = NaN. A minimum of zero is kept as +0.
 """
 from __future__ import annotations
@@ -35,7 +36,14 @@ def quantise(x):
         bad = ~np.isfinite(span)
         step = _bf16_value(_bf16_bits(span / np.float32(15)))
         step = np.where(bad | (step < 2.0 ** -126), 0.0, step)
-        q = np.floor((g - low[..., None]) / step[..., None] + 0.5)
+        # x − m as an unevaluated sum d + e; a half-way point has 13 bits, so d decides unless it is one
+        m = low[..., None]
+        d = g - m
+        e = np.where(np.abs(g) >= np.abs(m), (g - d) - m, g - (d + m))
+        q = np.zeros(g.shape)
+        for k in range(15):
+            half = (k + 0.5) * step[..., None]
+            q += (d > half) | ((d == half) & (e >= 0))
     q = np.where(step[..., None] > 0, q, 0.0)
     assert q.min() >= 0 and q.max() <= 15
     low = np.where(bad, np.nan, low + 0.0)  # a minimum of -0 is kept as +0
