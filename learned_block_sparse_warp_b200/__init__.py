@@ -444,7 +444,8 @@ class Kv4Cache:
     Tensors whose memory has moved since (resized in place) are checked again and followed. A captured step keeps the
     memory it was captured with."""
 
-    __slots__ = ("_k", "_v", "_block_table", "_dims", "_blocks", "_device", "_at", "_ref")
+    __slots__ = ("_k", "_v", "_block_table", "_dims", "_blocks", "_device", "_at", "_k_at", "_v_at", "_table_at",
+                 "_ref")
 
     def __init__(self, p: Params, k: torch.Tensor, v: torch.Tensor, block_table: Optional[torch.Tensor] = None):
         if k is None:
@@ -461,9 +462,12 @@ class Kv4Cache:
         shape = ((B, Hkv, self._blocks) if block_table is None else (n_pages, Hkv)) + (kv4_record_bytes(d),)
         at = (_arg(k, torch.uint8, shape, "k", dev), _arg(v, torch.uint8, shape, "v", dev),
               _opt(block_table, i32, (B, self._blocks), "block_table", dev))
-        # a struct of its own: a call on another thread may be using the last one
+        # a struct of its own, with its tensors: a call on another thread may be using the last one
+        c = sas_kv4_cache(*at, n_pages)
+        c.tensors = (k, v, block_table)
+        self._ref = ctypes.byref(c)
         self._k, self._v, self._block_table, self._at = k, v, block_table, at
-        self._ref = ctypes.byref(sas_kv4_cache(*at, n_pages))
+        self._k_at, self._v_at, self._table_at = k.data_ptr, v.data_ptr, None if block_table is None else block_table.data_ptr
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -482,14 +486,14 @@ class Kv4Cache:
 
     def of(self, p: Params):
         """(C struct, shapes of p), once p has been checked against the cache's shape and the current device."""
-        sh = _Kv4Shapes.of(p)
+        sh = p.__dict__.get("_shapes") or _Kv4Shapes.of(p)
         if self._dims != sh.cache:
             raise ValueError(f"cache: made for batch, n_kv_heads, head_dim, seq_len = {self._dims}, called with {sh.cache}")
         if self._device != _device():
             raise ValueError(f"cache: lies on cuda:{self._device}, the current device is cuda:{_device()}")
-        t = self._block_table
-        if (self._k.data_ptr(), self._v.data_ptr(), None if t is None else t.data_ptr()) != self._at:
-            self._bind(self._k, self._v, t)
+        k, v, table = self._at
+        if self._k_at() != k or self._v_at() != v or (table is not None and self._table_at() != table):
+            self._bind(self._k, self._v, self._block_table)
         return self._ref, sh
 
 
@@ -508,9 +512,10 @@ def empty_kv4_cache(p: Params, n_pages: Optional[int] = None, block_table: Optio
 def _tokens(t, name: str) -> int:
     if t is None:
         raise ValueError(f"{name}: missing")
-    if t.dim() != 4:
-        raise ValueError(f"{name}: expected [B, Hkv, T, d], got shape {tuple(t.shape)}")
-    return t.shape[2]
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name}: expected [B, Hkv, T, d], got shape {tuple(shape)}")
+    return shape[2]
 
 
 def sas_kv4_write(p: Params, cache: Kv4Cache, k, v, cache_len, new_len=None, stream=None) -> None:
@@ -671,21 +676,22 @@ def decode_step_scored(p: Params, q, kc, vc, kmean, cache_len, s, n_split: int, 
     sas_decode_combine(p, n_split, out["o_part"], out["lse_part"], out["o"], out["lse_o"], stream=stream)
 
 
-def _refuse_decode_kv4(p: Params, n_split: int, pointers) -> None:
-    """The rules of sas_decode_kv4 and of alignment, for steps that change something before that call."""
-    code = 0
-    if p.n_q_heads > 8 * p.n_kv_heads:
-        code = 2  # SAS_ERR_UNSUPPORTED
-    elif any(x & 15 for x in pointers) or not 1 <= n_split <= min(p.top_k + 1, 65535):
-        code = 1  # SAS_ERR_INVALID_ARG
-    elif (p.top_k + n_split) // n_split > 64 or p.batch * p.n_kv_heads * n_split >= 1 << 31:
-        code = 2
-    _check("sas_decode_kv4", code)
+def _refuse_decode_kv4(p: Params, n_split: int, bits: int) -> None:
+    """The rules of sas_decode_kv4 and of alignment, for steps that change something before that call. bits: all of the
+    step's pointers, or-ed."""
+    K, Hkv = p.top_k, p.n_kv_heads
+    if p.n_q_heads > 8 * Hkv:
+        _check("sas_decode_kv4", 2)  # SAS_ERR_UNSUPPORTED
+    if bits & 15 or not 1 <= n_split <= K + 1 or n_split > 65535:
+        _check("sas_decode_kv4", 1)  # SAS_ERR_INVALID_ARG
+    if K + n_split >= 65 * n_split or p.batch * Hkv * n_split >= 1 << 31:
+        _check("sas_decode_kv4", 2)
 
 
-def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream, more=()) -> None:
+def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: dict, select, stream, more: int = 0) -> None:
     """Select, split-K attention and merge over a 4-bit cache, every argument checked once and before the first
-    launch. select(c, cache, pointers..., stream) launches the selection, which takes the pointers `more` too."""
+    launch. select(c, cache, pointers..., stream) launches the selection, which takes other pointers too, or-ed in
+    `more`."""
     ref, sh = cache.of(p)
     dev, c, st = cache._device, sh.c, _stream_on(cache._device, stream)
     B, Hq, d = sh.q
@@ -696,7 +702,7 @@ def _steps_kv4(p: Params, q, cache: Kv4Cache, cache_len, s, n_split: int, out: d
     op = _arg(out["o_part"], f32, (B, Hq, n_split, d), "o_part", dev)
     xp = _arg(out["lse_part"], f32, (B, Hq, n_split), "lse_part", dev)
     yp, zp = _arg(out["o"], bf16, sh.q, "o", dev), _opt(out.get("lse_o"), f32, sh.lse_o, "lse_o", dev)
-    _refuse_decode_kv4(p, n_split, (qp, lp, sp, ip, ep, op, xp, yp, zp or 0, *more))
+    _refuse_decode_kv4(p, n_split, qp | lp | sp | ip | ep | op | xp | yp | (zp or 0) | more)
     select(c, ref, qp, lp, sp, ip, ep, st)
     _check("sas_decode_kv4", lib.sas_decode_kv4(c, qp, ref, lp, sp, ip, ep, n_split, op, xp, st))
     _check("sas_decode_combine", lib.sas_decode_combine(c, n_split, op, xp, yp, zp, st))
@@ -735,7 +741,7 @@ def decode_step_scored_kv4(p: Params, q, k_new, v_new, cache: Kv4Cache, kmean, c
         _check("sas_kv4_block_mean_keys", lib.sas_kv4_block_mean_keys(c, ref, 1, lp, None, kp, st))
         _check("sas_decode_select_scored", lib.sas_decode_select_scored(c, qp, kp, lp, sp, ip, ep, st))
 
-    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream, (new_k, new_v, kp))
+    _steps_kv4(p, q, cache, cache_len, s, n_split, out, select, stream, new_k | new_v | kp)
 
 
 class DecodeGraph:
