@@ -8,7 +8,7 @@
 // float) is stored as s = 0, m = NaN: it reads back as NaN, and attention rows
 // that reach it become NaN.
 //
-// Read: bf16(s·code + m), one rounding. Means: (1/64) Σ (s·code + m) in fp32.
+// Read: bf16(s·code + m), one rounding. Means: Σ s·(code/64) + Σ m/64 in fp32.
 //
 // The read is bound by the bytes it moves, write and means by the integer pipe
 // as well. Write and read give a tile of 16 tokens to a warp, the means a
@@ -376,13 +376,14 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
   return y;
 }
 
-// Nibbles 2 c and 2 c + 1 of a word as floats. A nibble at bit p is left where
-// it is: under the exponent of 2^(23 - p) it counts ones, and 2^(23 - p) comes
-// off exactly. Bits 20 and up are moved down by 12 first.
+// 1/64 of nibbles 2 c and 2 c + 1 of a word as floats: the share of a mean, which
+// keeps the sums of any finite keys in fp32's range. A nibble at bit p is left
+// where it is: under the exponent of 2^(17 - p) it counts 1/64s, and 2^(17 - p)
+// comes off exactly. Bits 20 and up are moved down by 12 first.
 __device__ __forceinline__ float2 nibble_pair(uint32_t w, int c) {
   const uint32_t x = 2 * c >= 5 ? w >> 12 : w, y = 2 * c + 1 >= 5 ? w >> 12 : w;
   const int px = 8 * c - (2 * c >= 5 ? 12 : 0), py = 8 * c + 4 - (2 * c + 1 >= 5 ? 12 : 0);
-  const uint32_t ex = uint32_t(127 + 23 - px) << 23, ey = uint32_t(127 + 23 - py) << 23;
+  const uint32_t ex = uint32_t(127 + 17 - px) << 23, ey = uint32_t(127 + 17 - py) << 23;
   return add_f32x2(make_float2(__uint_as_float(and_or(x, 15u << px, ex)), __uint_as_float(and_or(y, 15u << py, ey))),
                    make_float2(-__uint_as_float(ex), -__uint_as_float(ey)));
 }
@@ -413,7 +414,7 @@ __device__ __forceinline__ void mean_of(const uint8_t* rec, uint16_t* out) {
 #pragma unroll
     for (int i = 0; i < 2 * kTiles; ++i) {
       const float sf = __uint_as_float((j & 1) ? s[i][j / 2] & 0xffff0000u : s[i][j / 2] << 16);
-      low += __uint_as_float((j & 1) ? lo[i][j / 2] & 0xffff0000u : lo[i][j / 2] << 16);
+      low = fmaf(__uint_as_float((j & 1) ? lo[i][j / 2] & 0xffff0000u : lo[i][j / 2] << 16), 1.f / kBlock, low);
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[j][c] = fma_f32x2(nibble_pair(w[i][j], c), dup2(sf), acc[j][c]);
     }
@@ -437,9 +438,9 @@ __device__ __forceinline__ void mean_of(const uint8_t* rec, uint16_t* out) {
   // this lane has the N/8 channels from N/8 · g of its t's list
   const int c0 = g * (N / 8), ch = 32 * (c0 / 8) + 8 * t + c0 % 8;
   if (NG == 4)
-    *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_bf16x2(x[0] / kBlock, x[1] / kBlock), pack_bf16x2(x[2] / kBlock, x[3] / kBlock));
+    *reinterpret_cast<uint2*>(out + ch) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
   else
-    *reinterpret_cast<uint32_t*>(out + ch) = pack_bf16x2(x[0] / kBlock, x[1] / kBlock);
+    *reinterpret_cast<uint32_t*>(out + ch) = pack_bf16x2(x[0], x[1]);
 }
 
 // Candidate block `item` of [bh][block]: its K record, or -1 where the new
