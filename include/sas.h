@@ -350,9 +350,11 @@ SAS_API sas_status sas_decode_select_scored(const sas_params* p, const sas_bf16*
  *
  * The d channels of a token are cut into groups of 32. A group x keeps its
  * minimum m = min x and a step s, both bf16, and a 4-bit code per channel:
- *   s = bf16((max x − m) / 15), 0 if that is below 2^-126,
- *   code = floor((x − m) / s + 1/2) in 0..15 (0 where s = 0),
- * and stands for the values s·code + m, each within s/2 of x. A group whose
+ *   s = bf16((max x − m) / 15), the difference and the quotient rounded to
+ *       fp32 before, 0 if that is below 2^-126,
+ *   code = floor((x − m) / s + 1/2) in 0..15, exactly (0 where s = 0),
+ * and stands for the values s·code + m, each within s/2 of x (within 2^-122
+ * where s = 0). A group whose
  * range max − min is not a finite fp32 number (it holds a NaN or an infinity,
  * or overflows) is stored as s = 0, m = NaN and reads as NaN throughout. A
  * minimum of zero is stored as +0.

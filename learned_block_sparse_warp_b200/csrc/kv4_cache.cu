@@ -10,8 +10,9 @@
 //
 // Read: bf16(s·code + m), one rounding. Means: Σ s·(code/64) + Σ m/64 in fp32.
 //
-// The read is bound by the bytes it moves, write and means by the integer pipe
-// as well. Write and read give a tile of 16 tokens to a warp, the means a
+// The read is bound by the bytes it moves. Write and means are bound by nothing
+// alone: their integer instructions and the wait for their loads share the time
+// (the figures are at the kernels). Write and read give a tile of 16 tokens to a warp, the means a
 // record: enough independent 16-byte loads per lane that the few dependent ones
 // before them (length, page) are hidden by the multiprocessor's other warps.
 #include "kv4.cuh"
@@ -45,7 +46,7 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 // Two neighbouring lanes hold a group, 16 bf16 channels each. Every lane of the
 // warp takes part. Sixteen channels a lane rather than eight, because the
 // group's parameters cost as much as eight of its codes, and the arithmetic is
-// what bounds a long write.
+// most of a long write's instructions.
 //
 // The quotient (x − m)/s is formed as (x − m)·r with r = 1/s raised by 2^-20,
 // which outweighs the reciprocal's error: a value half-way between two levels
@@ -160,7 +161,9 @@ __device__ __forceinline__ int stage_unit(int unit) {
 // Warps of a write CTA. The bound of 28 warps per multiprocessor (72 registers)
 // measures best: writing 32K tokens and reading them back takes 56 us with it,
 // 68 at the 91 registers of the unbounded kernel. The write alone takes 34 us,
-// 5.2 TB/s; the integer pipe, at two thirds of its rate, bounds it.
+// 5.2 TB/s, 0.79 of a copy's rate. Of what it does the integer pipe is busiest,
+// at 66 % of its rate, 69 % of the cycles issue, and the loads of a tile are the
+// largest stall.
 constexpr int kWriteWarps = 4;
 
 // A token's codes, step and minimum to their places in a tile in global memory.
@@ -461,9 +464,10 @@ constexpr int kMeanWarps = 4;
 // One warp per candidate block. The record comes through shared memory, by ten
 // copies a lane: 32768 records of d = 128 take 41 us so, 4.1 TB/s, against 51 us
 // straight from global memory in registers and 42 us with a persistent grid and
-// a ring of two records a warp; 8192 take 11 us. What bounds it is the
-// arithmetic: 980 instructions a record, half of them on the half-rate integer
-// pipe.
+// a ring of two records a warp; 8192 take 11 us. Neither a pipe nor DRAM is at
+// its limit there: 980 instructions a record, half of them on the half-rate
+// integer pipe, keep that 54 % busy and 61 % of the cycles issuing, DRAM is at
+// 32 %, and the wait for the one record that a warp has is the largest stall.
 template <int D>
 __global__ void __launch_bounds__(32 * kMeanWarps, 28 / kMeanWarps) kv4_means_kernel(Kv4Args a, unsigned per, uint16_t* __restrict__ kmean) {
   constexpr int kRecord = Fmt<D>::kRecord;

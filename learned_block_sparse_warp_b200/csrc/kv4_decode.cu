@@ -770,12 +770,13 @@ struct Row {
 // One CTA per (sequence, KV head, split), or a cluster of CS. The blocks of
 // the split's run go round the cluster's warps.
 //
-// All 2048 blocks of 8 heads of d = 128 in 64 splits: 37.2 us, 4.5 TB/s of
+// All 2048 blocks of 8 heads of d = 128 in 64 splits: 36.9 us, 4.5 TB/s of
 // records. 1200 instructions a block, the integer pipe (ANDs, shifts, steps into
 // fp16) busy half of the time, and 512 CTAs on 148 multiprocessors, 3 on some
-// and 4 on others. 64 ragged rows, K = 64, in 9 splits: 14.1 us, most of it the
+// and 4 on others. 64 ragged rows, K = 64, in 9 splits: 14.2 us, most of it the
 // way to the first block. 4 CTAs of 128 registers a multiprocessor, against 3
-// of 168 in the one-launch form, whose registers the selection needs. Clusters
+// of 168 in the one-launch form, whose registers the selection needs. At d = 128
+// the bound of 128 spills 36 to 48 bytes a thread. Clusters
 // past one wave of CTAs cost more than they even out (128K 45.8 -> 52.9 us for
 // the step).
 template <int D, bool CLUSTER, bool OUT>
@@ -853,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_decode_split_kernel(Kv4Decode
 // them, a selection by every warp was not: three CTAs share a multiprocessor,
 // and their instructions count.
 //
-// 128 rows, K = 16 of 511 blocks, d = 128: 12.3 us (the bf16 cache's step 19.7),
-// 8 rows, K = 64 of 127: 9.8 us (15.0). It is a chain of latencies; alone, the
+// 128 rows, K = 16 of 511 blocks, d = 128: 12.2 us (the bf16 cache's step 19.7),
+// 8 rows, K = 64 of 127: 9.7 us (15.0). It is a chain of latencies; alone, the
 // picks are known after 3.6 us, the records after 4.4, the blocks done after
 // 8.8, the partials merged after 11.6. Selecting nothing would save 0.2 us, for
 // the rest is hidden by the other warps and the launches on either side.

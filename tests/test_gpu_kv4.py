@@ -1,8 +1,7 @@
 """GPU parity of the 4-bit KV cache: write, read, block means and decode against the fp64 oracle.
 
 Tolerances, before any run. Records are compared bit for bit: the step is two IEEE fp32 operations and a rounding,
-and a code differs from the definition only where (x - m)/s lies within 2^-20 of a half-way point without being one,
-which bf16 inputs of these scales cannot do.
+and the codes are those of the exact x - m.
   read   one rounding to bf16 (2^-8 of the value) after one to fp32.
   means  64 fp32 additions (64 * 2^-24 of the largest partial sum, at most the sum of |k|) and a rounding to bf16.
   decode the logits z are fp32 sums of at most 34 tensor-core accumulations, each off by 2^-23 of the largest partial
